@@ -81,9 +81,9 @@ def _rows_per_expert(case, seed):
 
 
 def _tiles(scales):
-    """[G, N, K/32] scale bytes as the product's tiles: [G, N/128, K/128, 32, 4, 4], 2^0 in the padding."""
+    """[G, N, K/32] scale bytes as the product's tiles: [G, N/128, K/128 (even), 32, 4, 4], 2^0 in the padding."""
     G, N, nb = scales.shape
-    nt, kt = -(-N // 128), -(-nb // 4)
+    nt, kt = -(-N // 128), 2 * -(-nb // 8)
     full = scales.new_full((G, nt * 128, kt * 4), 127)
     full[:, :N, :nb] = scales
     return full.view(G, nt, 4, 32, kt, 4).permute(0, 1, 4, 3, 2, 5).contiguous().view(-1)
