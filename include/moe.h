@@ -355,6 +355,116 @@ MOE_API moe_status_t moe_glm_layer_forward(const moe_config_t* cfg, const moe_gl
                                            void* y, int32_t* topk_ids_out, float* topk_w_out, void* ws,
                                            size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ *
+ * MXFP4 quantization and the MXFP4 x MXFP4 product
+ * ------------------------------------------------------------------------ */
+
+/* MXFP4 quantization of rows along K, the format of the MOE_W_MXFP4 weights:
+ *   x [rows, K] in dtype (moe_dtype_t; K a multiple of 32)
+ *   -> codes [rows, K/2] uint8 E2M1 (element 2i = low nibble of byte i),
+ *      scales [rows, K/32] uint8 E8M0: X + 127 for the block's scale 2^X, X the
+ *      smallest integer >= -127 with max |x| of the block <= 6 * 2^X (no
+ *      element saturates; -127 for an all-zero block); elements x / 2^X
+ *      rounded to nearest, ties to even.
+ * A block that holds an infinity or a NaN gets scale byte 255 (the E8M0 NaN)
+ * and zero codes.  rows = 0 is a no-op; rows <= 2^31. */
+MOE_API moe_status_t moe_quantize_mxfp4(int64_t rows, int32_t K, int32_t dtype, const void* x, uint8_t* codes,
+                                        uint8_t* scales, void* stream);
+
+/* The values of such codes: out [rows, K] in dtype, code * 2^(scale - 127),
+ * exact in bf16 and fp32 (scales above 252 may overflow to infinity); NaN where
+ * the scale byte is 255. */
+MOE_API moe_status_t moe_dequantize_mxfp4(int64_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales,
+                                          int32_t dtype, void* out, void* stream);
+
+/* Weight scales [G, N, K/32] relaid once for moe_mxfp4_linear: for every group,
+ * 128 rows and 128 elements of K a chunk of 512 bytes, byte
+ * 16 (n % 32) + 4 (n % 128 / 32) + b for row n's block b = 0..3 of the chunk;
+ * the chunks of a row block follow one another along K, an even number of them
+ * (padding along K is 127 = 2^0).  moe_mxfp4_weight_tiles_size bytes; (size_t)-1
+ * for sizes the product does not take. */
+MOE_API size_t moe_mxfp4_weight_tiles_size(int32_t G, int32_t N, int32_t K);
+MOE_API moe_status_t moe_mxfp4_weight_tiles(int32_t G, int32_t N, int32_t K, const uint8_t* scales, uint8_t* tiles,
+                                            void* stream);
+
+/* Linear layer with MXFP4 weights and MXFP4 activations, on the 4-bit
+ * block-scaled tensor cores (tcgen05.mma kind::mxf4, fp32 accumulation):
+ *   out[r, n] = sum_k q(x)[r, k] W_g[n, k] + bias[g, n]
+ * for the rows r of group g, [group_off[g], group_off[g+1]) (as expert_off;
+ * NULL with G = 1: all R rows), q the quantization of moe_quantize_mxfp4.
+ *   x [R, K] bf16, w_codes [G, N, K/2], w_tiles from moe_mxfp4_weight_tiles,
+ *   bias [G, N] bf16 or NULL -> out [R, N] bf16, or fp32 if out_f32 is 1.
+ * Rows that belong to no group are left as they are.
+ * 1 <= G <= 256, N a multiple of 16, K of 32.  ws:
+ * moe_mxfp4_linear_workspace_size bytes (the quantized activations). */
+MOE_API size_t moe_mxfp4_linear_workspace_size(int32_t G, int64_t R, int32_t N, int32_t K);
+MOE_API moe_status_t moe_mxfp4_linear(int32_t G, int64_t R, int32_t N, int32_t K, const void* x,
+                                      const int32_t* group_off, const uint8_t* w_codes, const uint8_t* w_tiles,
+                                      const void* bias, int32_t out_f32, void* out, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Training pass of the expert feed-forward block
+ * ------------------------------------------------------------------------ */
+
+/* Activation of the block: the layer's clipped SwiGLU (swiglu_limit and
+ * swiglu_alpha of the config) or SiLU(g) * u (the GLM4-MoE-Lite experts). */
+typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_SILU = 1 } moe_act_t;
+
+/* moe_expert_ffn that also keeps what the backward pass reads:
+ *   x_perm [R, D], expert_off [E+1] (R = T*k)
+ *   -> gu [R, 2, F] in dtype: row r holds g (biases added, before the clips),
+ *      then u; a bf16 value is rounded to nearest but never across a clip bound,
+ *      so that the backward pass sees on which side of the clip it was,
+ *      h [R, F] in dtype, y_perm [R, D] in dtype.
+ * Dense weights in dtype; each of the biases may be NULL (none).  h_split and
+ * MXFP4 weights: MOE_ERR_UNSUPPORTED.  With E = k = 1 it is a dense block.
+ * ws: moe_expert_ffn_train_workspace_size bytes (may be NULL if b_down is not). */
+MOE_API size_t moe_expert_ffn_train_workspace_size(const moe_config_t* cfg, int64_t T);
+MOE_API moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
+                                          const int32_t* expert_off, const moe_expert_weights_t* weights, void* gu,
+                                          void* h, void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of the expert parameters, same layouts as the parameters, in dtype
+ * or in fp32 (grad_f32 = 1).  A NULL pointer: not wanted; a bias gradient comes
+ * with its weight's. */
+typedef struct {
+  void* w_gate;     /* [E, F, D] */
+  void* w_up;       /* [E, F, D] */
+  void* w_down;     /* [E, D, F] */
+  void* b_gate;     /* [E, F] */
+  void* b_up;       /* [E, F] */
+  void* b_down;     /* [E, D] */
+  int32_t grad_f32;
+} moe_expert_grads_t;
+
+/* Backward pass of moe_expert_ffn_train: from dy_perm [R, D] (the gradient of
+ * y_perm) and the forward's x_perm, gu and h,
+ *   dh = dy Wd, dg = dh u' f'(g) where 0 <= g <= L, du = dh f(g') where |u| <= L
+ *     (zero elsewhere; f(a) = a sigmoid(alpha a), g' and u' the clipped values;
+ *      SiLU: no clips),
+ *   dx_perm [R, D] = dg Wg + du Wu in dtype (NULL: not wanted),
+ *   the weights' gradients dg^T x, du^T x, dy^T h over each expert's rows and the
+ *   biases' column sums, overwritten (zero for an expert without rows).
+ * bf16 layers: dg and du are rounded to bf16 before the products that read them
+ * (tensor-core operands); every sum is fp32.  fp32 layers: fp32 FMA throughout.
+ * The biases of `weights` are not read.  Deterministic.  T = 0 zeroes the
+ * gradients.  ws: moe_expert_ffn_backward_workspace_size bytes. */
+MOE_API size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T);
+MOE_API moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
+                                             const int32_t* expert_off, const moe_expert_weights_t* weights,
+                                             const void* gu, const void* h, const void* dy_perm, void* dx_perm,
+                                             const moe_expert_grads_t* grads, void* ws, size_t ws_bytes,
+                                             void* stream);
+
+/* Backward pass of moe_combine: dy [T, D] in dtype (the gradient of y), the
+ * forward's y_perm [T*k, D], row_of_slot [T, k] and topk_w [T, k]
+ *   -> dy_perm [T*k, D] in dtype: dy_perm[row_of_slot[t,j]] = topk_w[t,j] dy[t],
+ *      dtopk_w [T, k] fp32:       dtopk_w[t,j] = dy[t] . y_perm[row_of_slot[t,j]]. */
+MOE_API moe_status_t moe_combine_backward(const moe_config_t* cfg, int64_t T, const void* dy, const void* y_perm,
+                                          const int32_t* row_of_slot, const float* topk_w, void* dy_perm,
+                                          float* dtopk_w, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,7 @@ MOE_ERR_DEVICE_BOUNDS = 6
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_W_DENSE, MOE_W_MXFP4, MOE_W_MXFP4_A8 = 0, 1, 2
+MOE_ACT_SWIGLU, MOE_ACT_SILU = 0, 1
 
 SIZE_INVALID = ctypes.c_size_t(-1).value
 ABI_VERSION = 2
@@ -56,10 +57,17 @@ class MoeGlmParams(ctypes.Structure):
     ]
 
 
+class MoeExpertGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down")] + [
+        ("grad_f32", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoeConfig)
 _W = ctypes.POINTER(MoeExpertWeights)
 _GP = ctypes.POINTER(MoeGlmParams)
+_GR = ctypes.POINTER(MoeExpertGrads)
+_I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _ST = ctypes.c_int
 
@@ -88,6 +96,17 @@ SIGNATURES = {
     "moe_glm_workspace_size": (ctypes.c_size_t, [_CFG, _GP, _I64]),
     "moe_glm_router_topk": (_ST, [_CFG, _GP, _I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_glm_layer_forward": (_ST, [_CFG, _GP, _I64, _P, _P, _W, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_quantize_mxfp4": (_ST, [_I64, _I32, _I32, _P, _P, _P, _P]),
+    "moe_dequantize_mxfp4": (_ST, [_I64, _I32, _P, _P, _I32, _P, _P]),
+    "moe_mxfp4_weight_tiles_size": (ctypes.c_size_t, [_I32, _I32, _I32]),
+    "moe_mxfp4_weight_tiles": (_ST, [_I32, _I32, _I32, _P, _P, _P]),
+    "moe_mxfp4_linear_workspace_size": (ctypes.c_size_t, [_I32, _I64, _I32, _I32]),
+    "moe_mxfp4_linear": (_ST, [_I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P]),
+    "moe_expert_ffn_train_workspace_size": (ctypes.c_size_t, [_CFG, _I64]),
+    "moe_expert_ffn_train": (_ST, [_CFG, _I32, _I64, _P, _P, _W, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_expert_ffn_backward_workspace_size": (ctypes.c_size_t, [_CFG, _I64]),
+    "moe_expert_ffn_backward": (_ST, [_CFG, _I32, _I64, _P, _P, _W, _P, _P, _P, _P, _GR, _P, ctypes.c_size_t, _P]),
+    "moe_combine_backward": (_ST, [_CFG, _I64, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 _lock = threading.Lock()

@@ -453,6 +453,263 @@ def quantize_mxfp8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     return xq, sf
 
 
+# --------------------------------------------------------------------------- #
+# MXFP4 quantization and the MXFP4 x MXFP4 linear layer
+# --------------------------------------------------------------------------- #
+_DT_OF = {torch.bfloat16: _lib.MOE_BF16, torch.float32: _lib.MOE_F32}
+
+
+def quantize_mxfp4(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x [..., K] bf16 or fp32 -> (E2M1 codes [..., K/2] uint8, E8M0 scales [..., K/32] uint8), the
+    layout of MXFP4 expert weights (moe_quantize_mxfp4)."""
+    if x.dim() < 1 or x.dtype not in _DT_OF:
+        raise ValueError("quantize_mxfp4 takes a bf16 or fp32 tensor of at least one dimension")
+    K = x.shape[-1]
+    if K == 0 or K % 32:
+        raise ValueError(f"quantize_mxfp4: the last dimension ({K}) must be a positive multiple of 32")
+    lead = x.shape[:-1]
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(_lib.load().moe_quantize_mxfp4(x.numel() // K, K, _DT_OF[x.dtype], _p(x), _p(codes), _p(scales),
+                                              _stream(x.device)), "moe_quantize_mxfp4")
+    return codes, scales
+
+
+def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values of quantize_mxfp4's codes and scales, [..., K] in dtype (exact; NaN for scale byte 255)."""
+    if codes.dim() < 1 or codes.dtype != torch.uint8:
+        raise ValueError("dequantize_mxfp4 takes uint8 codes [..., K/2]")
+    if dtype not in _DT_OF:
+        raise ValueError("dequantize_mxfp4 gives bf16 or fp32")
+    K = 2 * codes.shape[-1]
+    if K == 0 or K % 32:
+        raise ValueError(f"dequantize_mxfp4: K = {K} must be a positive multiple of 32")
+    _want("scales", scales, (*codes.shape[:-1], K // 32), torch.uint8, codes.device)
+    out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
+    with torch.cuda.device(codes.device):
+        _check(_lib.load().moe_dequantize_mxfp4(out.numel() // K, K, _p(codes), _p(scales), _DT_OF[dtype], _p(out),
+                                                _stream(codes.device)), "moe_dequantize_mxfp4")
+    return out
+
+
+@dataclasses.dataclass
+class Mxfp4Weights:
+    """Weights of ``mxfp4_linear``: E2M1 codes [G, N, K/2] and the scales as moe_mxfp4_weight_tiles lays
+    them out (flat uint8).  ``mxfp4_weights`` makes them from codes and scales."""
+    codes: torch.Tensor
+    tiles: torch.Tensor
+
+
+def _mxfp4_sizes(codes: torch.Tensor) -> Tuple[int, int, int]:
+    if codes.dim() != 3 or codes.dtype != torch.uint8:
+        raise ValueError("MXFP4 weight codes are uint8 [G, N, K/2]")
+    return codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+
+
+def mxfp4_weights(codes: torch.Tensor, scales: torch.Tensor) -> Mxfp4Weights:
+    """codes [G, N, K/2], scales [G, N, K/32] (quantize_mxfp4's, or MXFP4 expert weights) -> Mxfp4Weights."""
+    G, N, K = _mxfp4_sizes(codes)
+    L = _lib.load()
+    _want("scales", scales, (G, N, K // 32), torch.uint8, codes.device)
+    n = _size(L.moe_mxfp4_weight_tiles_size(G, N, K), "moe_mxfp4_weight_tiles_size")
+    tiles = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    with torch.cuda.device(codes.device):
+        _check(L.moe_mxfp4_weight_tiles(G, N, K, _p(scales), _p(tiles), _stream(codes.device)),
+               "moe_mxfp4_weight_tiles")
+    return Mxfp4Weights(codes, tiles)
+
+
+def check_mxfp4_linear_args(x, w: Mxfp4Weights, bias=None, group_off=None, y=None, out_f32: bool = False) -> int:
+    """x [R, K] bf16, w from ``mxfp4_weights``, bias [G, N] bf16 and group_off [G+1] int32 when given
+    (group_off is required for G > 1), y [R, N] bf16 (fp32 with out_f32) when given.  Returns R."""
+    G, N, K = _mxfp4_sizes(w.codes)
+    R = _rows("x", x)
+    dev = x.device
+    _want("x", x, (R, K), torch.bfloat16)
+    _want("w.codes", w.codes, w.codes.shape, torch.uint8, dev)
+    n = _size(_lib.load().moe_mxfp4_weight_tiles_size(G, N, K), "moe_mxfp4_weight_tiles_size")
+    _want("w.tiles", w.tiles, (n,), torch.uint8, dev)
+    if bias is not None:
+        _want("bias", bias, (G, N), torch.bfloat16, dev)
+    if group_off is not None:
+        _want("group_off", group_off, (G + 1,), torch.int32, dev)
+    elif G != 1:
+        raise ValueError("group_off is required for more than one group of weights")
+    if y is not None:
+        _want("y", y, (R, N), torch.float32 if out_f32 else torch.bfloat16, dev)
+    return R
+
+
+def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] = None,
+                 group_off: Optional[torch.Tensor] = None, out_f32: bool = False, y: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[r] = q(x)[r] W_g^T + bias_g for the rows r of group g (group_off as expert_off; all rows if None),
+    x quantized to MXFP4 in the call: 4-bit x 4-bit products on the block-scaled tensor cores
+    (moe_mxfp4_linear)."""
+    R = check_mxfp4_linear_args(x, w, bias, group_off, y, out_f32)
+    G, N, K = _mxfp4_sizes(w.codes)
+    L, dev = _lib.load(), x.device
+    if y is None:
+        y = torch.empty((R, N), dtype=torch.float32 if out_f32 else torch.bfloat16, device=dev)
+    if ws is None:
+        n = _size(L.moe_mxfp4_linear_workspace_size(G, R, N, K), "moe_mxfp4_linear_workspace_size")
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    with torch.cuda.device(dev):
+        _check(L.moe_mxfp4_linear(G, R, N, K, _p(x), _p(group_off), _p(w.codes), _p(w.tiles), _p(bias),
+                                  1 if out_f32 else 0, _p(y), _p(ws), ws.numel() * ws.element_size(), _stream(dev)),
+               "moe_mxfp4_linear")
+    return y
+
+
+def quantize_experts(cfg: MoeConfig, w: ExpertWeights, wfmt: str = "mxfp4") -> Tuple[MoeConfig, ExpertWeights]:
+    """Dense bf16 expert weights -> (config, weights) of the same layer with MXFP4 weights (wfmt "mxfp4"
+    or "mxfp4_a8"); biases stay as they are."""
+    if cfg.wfmt != _lib.MOE_W_DENSE or cfg.dtype != _lib.MOE_BF16:
+        raise ValueError("quantize_experts takes dense bf16 expert weights")
+    if wfmt not in ("mxfp4", "mxfp4_a8"):
+        raise ValueError(f"wfmt {wfmt!r}: 'mxfp4' or 'mxfp4_a8'")
+    check_expert_weights(cfg, w)
+    new = MoeConfig(cfg.hidden_size, cfg.intermediate_size, cfg.num_local_experts, cfg.num_experts_per_tok,
+                    cfg.swiglu_limit, cfg.swiglu_alpha, cfg.dtype, _WF[wfmt], cfg.y_f32, 0)
+    _check(_lib.load().moe_config_check(ctypes.byref(new)), "moe_config_check")
+    (cg, sg), (cu, su), (cd, sd) = (quantize_mxfp4(t) for t in (w.w_gate, w.w_up, w.w_down))
+    return new, ExpertWeights(cg, cu, cd, w.b_gate, w.b_up, w.b_down, sg, su, sd)
+
+
+# --------------------------------------------------------------------------- #
+# training pass of the expert block
+# --------------------------------------------------------------------------- #
+_ACT = {"swiglu": _lib.MOE_ACT_SWIGLU, "silu": _lib.MOE_ACT_SILU}
+
+
+def _act_code(act: str) -> int:
+    if act not in _ACT:
+        raise ValueError(f"act {act!r}: 'swiglu' (the layer's clipped SwiGLU) or 'silu'")
+    return _ACT[act]
+
+
+def check_ffn_train_args(cfg: MoeConfig, x_perm, expert_off, w: ExpertWeights, gu=None, h=None, dy_perm=None) -> int:
+    """x_perm [R, D] with R = T*k, expert_off [E+1] int32, dense weights in the layer dtype (each bias
+    may be None); for the backward pass gu [R, 2, F], h [R, F] and dy_perm [R, D].  Returns T."""
+    D, F, E, k = cfg.hidden_size, cfg.intermediate_size, cfg.num_local_experts, cfg.num_experts_per_tok
+    dt = torch_dtype(cfg)
+    if cfg.wfmt != _lib.MOE_W_DENSE:
+        raise ValueError("the training pass takes dense expert weights")
+    R = _rows("x_perm", x_perm)
+    if R % k:
+        raise ValueError(f"x_perm has {R} rows, not a multiple of k = {k}")
+    dev = x_perm.device
+    _want("x_perm", x_perm, (R, D), dt)
+    _want("expert_off", expert_off, (E + 1,), torch.int32, dev)
+    _want("w_gate", w.w_gate, (E, F, D), dt, dev)
+    _want("w_up", w.w_up, (E, F, D), dt, dev)
+    _want("w_down", w.w_down, (E, D, F), dt, dev)
+    for name, t, n in (("b_gate", w.b_gate, F), ("b_up", w.b_up, F), ("b_down", w.b_down, D)):
+        if t is not None:
+            _want(name, t, (E, n), dt, dev)
+    if dy_perm is not None:
+        _want("gu", gu, (R, 2, F), dt, dev)
+        _want("h", h, (R, F), dt, dev)
+        _want("dy_perm", dy_perm, (R, D), dt, dev)
+    return R // k
+
+
+def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Tensor, weights: ExpertWeights,
+                     act: str = "swiglu") -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """expert_ffn that also keeps the pre-activations: (gu [R, 2, F], h [R, F], y_perm [R, D]).
+    act: "swiglu" (the layer's clipped SwiGLU) or "silu"; biases may be None."""
+    code = _act_code(act)
+    T = check_ffn_train_args(cfg, x_perm, expert_off, weights)
+    L, R, dev, dt = _lib.load(), x_perm.shape[0], x_perm.device, x_perm.dtype
+    gu = torch.empty((R, 2, cfg.intermediate_size), dtype=dt, device=dev)
+    h = torch.empty((R, cfg.intermediate_size), dtype=dt, device=dev)
+    y = torch.empty((R, cfg.hidden_size), dtype=dt, device=dev)
+    ws, nws = None, 0
+    if weights.b_down is None:
+        nws = _size(L.moe_expert_ffn_train_workspace_size(ctypes.byref(cfg), T), "moe_expert_ffn_train_workspace_size")
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    wst = weights.c_struct()
+    with torch.cuda.device(dev):
+        _check(L.moe_expert_ffn_train(ctypes.byref(cfg), code, T, _p(x_perm), _p(expert_off), ctypes.byref(wst),
+                                      _p(gu), _p(h), _p(y), _p(ws), nws, _stream(dev)), "moe_expert_ffn_train")
+    return gu, h, y
+
+
+@dataclasses.dataclass
+class ExpertGrads:
+    """Gradients of the expert parameters, laid out as the parameters (moe_expert_grads_t)."""
+    w_gate: torch.Tensor
+    w_up: torch.Tensor
+    w_down: torch.Tensor
+    b_gate: Optional[torch.Tensor] = None
+    b_up: Optional[torch.Tensor] = None
+    b_down: Optional[torch.Tensor] = None
+
+    def c_struct(self) -> _lib.MoeExpertGrads:
+        ts = (self.w_gate, self.w_up, self.w_down, self.b_gate, self.b_up, self.b_down)
+        f32 = any(t is not None and t.dtype == torch.float32 for t in ts)
+        return _lib.MoeExpertGrads(*(None if t is None else t.data_ptr() for t in ts), 1 if f32 else 0)
+
+
+def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Tensor, weights: ExpertWeights,
+                        gu: torch.Tensor, h: torch.Tensor, dy_perm: torch.Tensor, act: str = "swiglu",
+                        grad_f32: bool = False, need_dx: bool = True, grads: Optional[ExpertGrads] = None,
+                        ws: Optional[torch.Tensor] = None) -> Tuple[Optional[torch.Tensor], ExpertGrads]:
+    """Backward pass of expert_ffn_train: (dx_perm [R, D] or None, ExpertGrads).  Bias gradients come for
+    the biases that `weights` has.  grad_f32: the parameters' gradients in fp32.  `grads` are buffers to
+    overwrite (same layouts, one dtype), else new ones."""
+    code = _act_code(act)
+    if dy_perm is None:
+        raise ValueError("dy_perm is required")
+    T = check_ffn_train_args(cfg, x_perm, expert_off, weights, gu, h, dy_perm)
+    L, dev = _lib.load(), x_perm.device
+    D, F, E = cfg.hidden_size, cfg.intermediate_size, cfg.num_local_experts
+    gdt = torch.float32 if grad_f32 else torch_dtype(cfg)
+    has_bias = [b is not None for b in (weights.b_gate, weights.b_up, weights.b_down)]
+    if grads is None:
+        new = lambda *s: torch.empty(s, dtype=gdt, device=dev)  # noqa: E731
+        grads = ExpertGrads(new(E, F, D), new(E, F, D), new(E, D, F), new(E, F) if has_bias[0] else None,
+                            new(E, F) if has_bias[1] else None, new(E, D) if has_bias[2] else None)
+    else:
+        for name, t, shape in (("grads.w_gate", grads.w_gate, (E, F, D)), ("grads.w_up", grads.w_up, (E, F, D)),
+                               ("grads.w_down", grads.w_down, (E, D, F))):
+            _want(name, t, shape, gdt, dev)
+        for name, t, n in (("grads.b_gate", grads.b_gate, F), ("grads.b_up", grads.b_up, F),
+                           ("grads.b_down", grads.b_down, D)):
+            if t is not None:
+                _want(name, t, (E, n), gdt, dev)
+    dx = torch.empty_like(x_perm) if need_dx else None
+    nws = _size(L.moe_expert_ffn_backward_workspace_size(ctypes.byref(cfg), T),
+                "moe_expert_ffn_backward_workspace_size")
+    if ws is None:
+        ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    wst, gst = weights.c_struct(), grads.c_struct()
+    with torch.cuda.device(dev):
+        _check(L.moe_expert_ffn_backward(ctypes.byref(cfg), code, T, _p(x_perm), _p(expert_off), ctypes.byref(wst),
+                                         _p(gu), _p(h), _p(dy_perm), _p(dx), ctypes.byref(gst), _p(ws),
+                                         ws.numel() * ws.element_size(), _stream(dev)), "moe_expert_ffn_backward")
+    return dx, grads
+
+
+def combine_backward(cfg: MoeConfig, dy: torch.Tensor, y_perm: torch.Tensor, row_of_slot: torch.Tensor,
+                     topk_w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Backward pass of combine: dy [T, D] (layer dtype) -> (dy_perm [T*k, D], dtopk_w [T, k] fp32)."""
+    T = check_combine_args(cfg, y_perm, row_of_slot, topk_w)
+    dev = y_perm.device
+    _want("dy", dy, (T, cfg.hidden_size), torch_dtype(cfg), dev)
+    dy_perm = torch.empty_like(y_perm)
+    dw = torch.empty_like(topk_w)
+    with torch.cuda.device(dev):
+        _check(_lib.load().moe_combine_backward(ctypes.byref(cfg), T, _p(dy), _p(y_perm), _p(row_of_slot), _p(topk_w),
+                                                _p(dy_perm), _p(dw), _stream(dev)), "moe_combine_backward")
+    return dy_perm, dw
+
+
 def last_device_error() -> int:
     """Reads and clears the device error word (synchronises); returns a status code."""
     return _lib.load().moe_last_device_error()
@@ -510,6 +767,11 @@ class MoELayer:
             layer_forward(self.cfg, x, self.w_router, self.b_router, self.experts, y=y, ws=ws,
                           topk_ids=topk_ids, topk_w=topk_w, _weights_checked=True)
         return g.replay, y
+
+    def quantized(self, wfmt: str = "mxfp4") -> "MoELayer":
+        """The same layer with its dense bf16 expert weights quantized to MXFP4 (``quantize_experts``)."""
+        cfg, experts = quantize_experts(self.cfg, self.experts, wfmt)
+        return MoELayer(cfg, self.w_router, self.b_router, experts)
 
     def run_host_batches(self, xs_host, ys_host) -> None:
         """Run the layer on a sequence of pinned host batches, results into pinned host buffers.

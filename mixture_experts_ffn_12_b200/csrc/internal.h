@@ -123,6 +123,42 @@ cudaError_t decode_layer(const Launch& L, int64_t T, int D, int F, int E, int k,
                          int h_halves, bool out_f32, void* y, int32_t* ids_out, float* w_out, float* logits, int* cnt,
                          float* part, void* h, float* ys);
 
+// MXFP4 quantization and product (mxfp4_quant.cuh, grouped_gemm_mx4.cuh).  Scale tiles:
+// 512-byte chunks of 128 rows x 128 elements, mx4_chunks(K) a row block.
+cudaError_t mx4_quant_rows(const Launch& L, bool bf16, int64_t rows, int K, const void* x, uint8_t* codes,
+                           uint8_t* scales);
+cudaError_t mx4_dequant_rows(const Launch& L, bool bf16, int64_t rows, int K, const uint8_t* codes,
+                             const uint8_t* scales, void* out);
+cudaError_t mx4_scale_tiles(const Launch& L, int G, int N, int K, const uint8_t* scales, uint8_t* tiles);
+int64_t mx4_row_blocks(int64_t R, int G);
+cudaError_t mx4_quant_tiles(const Launch& L, int64_t R, int K, const void* x, const int32_t* off, int G,
+                            uint8_t* codes, uint8_t* tiles);
+// out [R, N] (bf16, or fp32 if out_f32) = A W_g^T + bias_g; off null: one group; bias may be null.
+cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const uint8_t* codes, const uint8_t* tiles,
+                        const int32_t* off, const uint8_t* w_codes, const uint8_t* w_tiles, const void* bias,
+                        bool out_f32, void* out);
+
+// Training pass of the expert block (ffn_backward.cuh).  Activation: gate_lo = 0 for the
+// clipped SwiGLU; gate_lo = -inf, limit = inf, alpha = 1 for SiLU.
+struct Activation {
+  float limit, alpha, gate_lo;
+};
+// gate/up projections storing gu [R, 2, F] and h [R, F]; w.b_gate / w.b_up may be null.
+cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
+                               const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
+                               void* h);
+struct ExpertGrads {
+  void *w_gate, *w_up, *w_down, *b_gate, *b_up, *b_down;   // each may be null
+};
+// dgu [R, 2, F] scratch in the layer dtype; dx may be null; gradients of the weights in the
+// layer dtype, or fp32 if grad_f32.
+cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
+                            const int32_t* expert_off, const ExpertWeights& w, const Activation& act, const void* gu,
+                            const void* h, const void* dy, void* dgu, void* dx, const ExpertGrads& grads,
+                            bool grad_f32);
+cudaError_t combine_backward(const Launch& L, bool bf16, int64_t T, int D, int k, const void* dy, const void* y_perm,
+                             const int32_t* row_of_slot, const float* w, void* dy_perm, float* dw);
+
 cudaError_t read_and_clear_device_error(int* bits);
 
 }  // namespace moe

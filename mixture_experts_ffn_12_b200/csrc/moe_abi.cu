@@ -11,6 +11,7 @@
 #include "router_permute_combine.cuh"
 #include "gemm_launch.cuh"
 #include "glm_variant.cuh"
+#include "train_launch.cuh"
 
 namespace {
 
@@ -387,6 +388,38 @@ GlmLayout glm_layout(const moe_config_t* c, const moe_glm_params_t* p, int64_t T
   L.total = o;
   return L;
 }
+
+// ---------------------------------------------------------------------------
+// MXFP4 product, training pass of the expert block
+// ---------------------------------------------------------------------------
+bool check_mx4(int32_t K) { return K > 0 && K % 32 == 0 && K <= (1 << 20); }
+bool check_mx4_weights(int32_t G, int32_t N, int32_t K) {
+  return check_mx4(K) && G >= 1 && G <= 256 && N > 0 && N % 16 == 0 && N <= (1 << 20);
+}
+
+// Workspace of moe_mxfp4_linear: the activations' codes and scale tiles.
+struct LinearLayout {
+  size_t codes, tiles, total;
+};
+LinearLayout linear_layout(int32_t G, int64_t R, int32_t K) {
+  LinearLayout L{};
+  L.tiles = align256(size_t(R) * (K / 2));
+  L.total = L.tiles + size_t(moe::mx4_row_blocks(R, G)) * moe::mx4_chunks(K) * 512;
+  return L;
+}
+
+moe_status_t check_train(const moe_config_t* c, int32_t act) {
+  const moe_status_t s = check_cfg(c);
+  if (s != MOE_OK) return s;
+  if (act != MOE_ACT_SWIGLU && act != MOE_ACT_SILU) return MOE_ERR_INVALID_ARG;
+  if (c->wfmt != MOE_W_DENSE || c->h_split != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+moe::Activation activation(const moe_config_t* c, int32_t act) {
+  if (act == MOE_ACT_SILU) return moe::Activation{INFINITY, 1.0f, -INFINITY};
+  return moe::Activation{c->swiglu_limit, c->swiglu_alpha, 0.0f};
+}
+bool opt_ok(const void* p) { return p == nullptr || aligned16(p); }
 
 // moe_layer_forward with MXFP4 weights and MXFP8 activations (arguments already checked)
 moe_status_t layer_forward_a8(const moe_config_t* cfg, const Launch& L, int64_t T, const void* x,
@@ -779,6 +812,158 @@ moe_status_t moe_glm_layer_forward(const moe_config_t* cfg, const moe_glm_params
       return MOE_ERR_CUDA;
   }
   return cuda_status(moe::combine_slots_shared(L, out_bf16(cfg), T, D, k, ys, ysh, y));
+}
+
+moe_status_t moe_quantize_mxfp4(int64_t rows, int32_t K, int32_t dtype, const void* x, uint8_t* codes,
+                                uint8_t* scales, void* stream) {
+  if (rows < 0 || rows > (int64_t(1) << 31) || !check_mx4(K)) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!ptr_ok(x) || !ptr_ok(codes) || !ptr_ok(scales)) return MOE_ERR_INVALID_ARG;
+  Launch L;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  return cuda_status(moe::mx4_quant_rows(L, dtype == MOE_BF16, rows, K, x, codes, scales));
+}
+
+moe_status_t moe_dequantize_mxfp4(int64_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales, int32_t dtype,
+                                  void* out, void* stream) {
+  if (rows < 0 || rows > (int64_t(1) << 31) || !check_mx4(K)) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!ptr_ok(codes) || !ptr_ok(scales) || !ptr_ok(out)) return MOE_ERR_INVALID_ARG;
+  Launch L;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  return cuda_status(moe::mx4_dequant_rows(L, dtype == MOE_BF16, rows, K, codes, scales, out));
+}
+
+size_t moe_mxfp4_weight_tiles_size(int32_t G, int32_t N, int32_t K) {
+  if (!check_mx4_weights(G, N, K)) return size_t(-1);
+  return size_t(G) * ((N + 127) / 128) * moe::mx4_chunks(K) * 512;
+}
+
+moe_status_t moe_mxfp4_weight_tiles(int32_t G, int32_t N, int32_t K, const uint8_t* scales, uint8_t* tiles,
+                                    void* stream) {
+  if (!check_mx4_weights(G, N, K) || !ptr_ok(scales) || !ptr_ok(tiles)) return MOE_ERR_INVALID_ARG;
+  Launch L;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  return cuda_status(moe::mx4_scale_tiles(L, G, N, K, scales, tiles));
+}
+
+size_t moe_mxfp4_linear_workspace_size(int32_t G, int64_t R, int32_t N, int32_t K) {
+  if (!check_mx4_weights(G, N, K) || R < 0 || R >= (int64_t(1) << 31)) return size_t(-1);
+  return R == 0 ? 0 : linear_layout(G, R, K).total;
+}
+
+moe_status_t moe_mxfp4_linear(int32_t G, int64_t R, int32_t N, int32_t K, const void* x, const int32_t* group_off,
+                              const uint8_t* w_codes, const uint8_t* w_tiles, const void* bias, int32_t out_f32,
+                              void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!check_mx4_weights(G, N, K) || R < 0 || R >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+  if (out_f32 != 0 && out_f32 != 1) return MOE_ERR_INVALID_ARG;
+  if (group_off == nullptr && G != 1) return MOE_ERR_INVALID_ARG;
+  if (R == 0) return MOE_OK;
+  if (!ptr_ok(x) || !opt_ok(group_off) || !ptr_ok(w_codes) || !ptr_ok(w_tiles) || !opt_ok(bias) || !ptr_ok(out))
+    return MOE_ERR_INVALID_ARG;
+  const LinearLayout LY = linear_layout(G, R, K);
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < LY.total) return MOE_ERR_WORKSPACE;
+  Launch L;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  uint8_t* codes = static_cast<uint8_t*>(ws) + LY.codes;
+  uint8_t* tiles = static_cast<uint8_t*>(ws) + LY.tiles;
+  if (moe::mx4_quant_tiles(L, R, K, x, group_off, G, codes, tiles) != cudaSuccess) return MOE_ERR_CUDA;
+  return cuda_status(
+      moe::mx4_product(L, R, N, K, G, codes, tiles, group_off, w_codes, w_tiles, bias, out_f32 != 0, out));
+}
+
+size_t moe_expert_ffn_train_workspace_size(const moe_config_t* cfg, int64_t T) {
+  if (check_train(cfg, MOE_ACT_SWIGLU) != MOE_OK || !check_T(T, cfg->num_experts_per_tok)) return size_t(-1);
+  return align256(size_t(cfg->num_local_experts) * cfg->hidden_size * elem_size(cfg));
+}
+
+moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
+                                  const int32_t* expert_off, const moe_expert_weights_t* weights, void* gu, void* h,
+                                  void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t s = check_train(cfg, act);
+  if (s != MOE_OK) return s;
+  if (!check_T(T, cfg->num_experts_per_tok)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ptr_ok(x_perm) || !ptr_ok(expert_off) || !ptr_ok(gu) || !ptr_ok(h) || !ptr_ok(y_perm) || weights == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!ptr_ok(weights->w_gate) || !ptr_ok(weights->w_up) || !ptr_ok(weights->w_down) || !opt_ok(weights->b_gate) ||
+      !opt_ok(weights->b_up) || !opt_ok(weights->b_down))
+    return MOE_ERR_INVALID_ARG;
+  const bool bf16 = cfg->dtype == MOE_BF16;
+  const int D = cfg->hidden_size, F = cfg->intermediate_size, E = cfg->num_local_experts;
+  const int64_t R = T * cfg->num_experts_per_tok;
+  moe::ExpertWeights w = to_internal(weights);
+  Launch L;
+  if (weights->b_down == nullptr) {   // the down projection's epilogue reads a bias: zeros
+    const size_t need = align256(size_t(E) * D * elem_size(cfg));
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, need, L.stream) != cudaSuccess) return MOE_ERR_CUDA;
+    w.b_down = ws;
+  } else if (!get_launch(stream, &L)) {
+    return MOE_ERR_CUDA;
+  }
+  if (moe::expert_gateup_save(L, bf16, R, D, F, E, x_perm, expert_off, w, activation(cfg, act), gu, h) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return cuda_status(moe::expert_down(L, bf16, R, D, F, E, h, expert_off, w, nullptr, nullptr, y_perm));
+}
+
+size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T) {
+  if (check_train(cfg, MOE_ACT_SWIGLU) != MOE_OK || !check_T(T, cfg->num_experts_per_tok)) return size_t(-1);
+  return size_t(T) * cfg->num_experts_per_tok * 2 * cfg->intermediate_size * elem_size(cfg);
+}
+
+moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
+                                     const int32_t* expert_off, const moe_expert_weights_t* weights, const void* gu,
+                                     const void* h, const void* dy_perm, void* dx_perm,
+                                     const moe_expert_grads_t* grads, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t s = check_train(cfg, act);
+  if (s != MOE_OK) return s;
+  if (!check_T(T, cfg->num_experts_per_tok) || grads == nullptr) return MOE_ERR_INVALID_ARG;
+  const bool bf16 = cfg->dtype == MOE_BF16;
+  const int D = cfg->hidden_size, F = cfg->intermediate_size, E = cfg->num_local_experts;
+  if (grads->grad_f32 != 0 && grads->grad_f32 != 1) return MOE_ERR_INVALID_ARG;
+  void* const gp[6] = {grads->w_gate, grads->w_up, grads->w_down, grads->b_gate, grads->b_up, grads->b_down};
+  for (int i = 0; i < 6; ++i)
+    if (!opt_ok(gp[i]) || (i >= 3 && gp[i] != nullptr && gp[i - 3] == nullptr)) return MOE_ERR_INVALID_ARG;
+  Launch L;
+  if (T == 0) {   // no rows: every gradient asked for is zero
+    if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+    const size_t gs = (bf16 && grads->grad_f32 == 0) ? 2 : 4;
+    const size_t n[6] = {size_t(E) * F * D, size_t(E) * F * D, size_t(E) * D * F, size_t(E) * F, size_t(E) * F,
+                         size_t(E) * D};
+    for (int i = 0; i < 6; ++i)
+      if (gp[i] != nullptr && cudaMemsetAsync(gp[i], 0, n[i] * gs, L.stream) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!ptr_ok(x_perm) || !ptr_ok(expert_off) || !ptr_ok(gu) || !ptr_ok(h) || !ptr_ok(dy_perm) || !opt_ok(dx_perm) ||
+      weights == nullptr || !ptr_ok(weights->w_gate) || !ptr_ok(weights->w_up) || !ptr_ok(weights->w_down))
+    return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < moe_expert_ffn_backward_workspace_size(cfg, T))
+    return MOE_ERR_WORKSPACE;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  const moe::ExpertGrads gr{gp[0], gp[1], gp[2], gp[3], gp[4], gp[5]};
+  return cuda_status(moe::expert_backward(L, bf16, T * cfg->num_experts_per_tok, D, F, E, x_perm, expert_off,
+                                          to_internal(weights), activation(cfg, act), gu, h, dy_perm, ws, dx_perm, gr,
+                                          grads->grad_f32 != 0));
+}
+
+moe_status_t moe_combine_backward(const moe_config_t* cfg, int64_t T, const void* dy, const void* y_perm,
+                                  const int32_t* row_of_slot, const float* topk_w, void* dy_perm, float* dtopk_w,
+                                  void* stream) {
+  const moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  if (!check_T(T, cfg->num_experts_per_tok)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ptr_ok(dy) || !ptr_ok(y_perm) || !ptr_ok(row_of_slot) || !ptr_ok(topk_w) || !ptr_ok(dy_perm) ||
+      !ptr_ok(dtopk_w))
+    return MOE_ERR_INVALID_ARG;
+  Launch L;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  return cuda_status(moe::combine_backward(L, cfg->dtype == MOE_BF16, T, cfg->hidden_size, cfg->num_experts_per_tok,
+                                           dy, y_perm, row_of_slot, topk_w, dy_perm, dtopk_w));
 }
 
 }  // extern "C"

@@ -1,0 +1,277 @@
+// MXFP4 quantization: rows of bf16 or fp32 to E2M1 codes with one E8M0 scale per 32
+// elements along K, and back.
+//
+// For a block b of 32 consecutive elements of a row
+//   X = the smallest integer >= -127 with max |b| <= 6 * 2^X   (6 = the largest E2M1 value,
+//       so no element saturates; -127 for an all-zero block),
+//   code = RNE to E2M1 of b / 2^X,   scale byte = X + 127,
+// and a block that holds an infinity or a NaN gets scale byte 255 (the E8M0 NaN) and
+// zero codes, so that it reads back as NaN instead of as a wrong number.
+//
+// Bound by memory: 2 (bf16) or 4 (fp32) bytes read and 0.53 written an element.  Four
+// lanes share a block (8 elements each, one or two 16-byte loads): every load and store
+// of a warp is contiguous, and the block maximum takes two shuffles.
+//
+// Scale layouts.  "Rows": [rows, K/32], what the MXFP4 expert weights of the layer use.
+// "Tiles": what the 4-bit x 4-bit product reads: for every 128 rows (counted from the
+// start of a group of rows) and every 128 elements of K one 512-byte chunk, in which
+// byte 16 (r % 32) + 4 (r % 128 / 32) + b holds row r's scale of block b = 0..3 -- the
+// 32-lane x 16-byte image that tcgen05.cp copies to TMEM.  The chunks of a row block are
+// consecutive along K and padded to an even number (one pipeline stage of the product
+// covers 256 elements); padding along K holds 127 (2^0: it scales codes that read as
+// zero), padding rows are never used.
+#pragma once
+
+#include "grouped_gemm_mx8.cuh"
+
+namespace moe {
+
+// 128-element chunks of a scale tile row, an even number.
+__host__ __device__ constexpr int mx4_chunks(int K) { return 2 * ((K + 255) / 256); }
+
+// The block scale exponent from the largest |x| as fp32 bits (finite): 6 = 1.5 * 2^2.
+__device__ __forceinline__ int mx4_exponent(uint32_t amax_bits) {
+  const int ef = static_cast<int>(amax_bits >> 23);
+  if (ef == 0) return -127;
+  return max(-127, (ef - 127) - 2 + ((amax_bits & 0x7FFFFFu) > 0x400000u ? 1 : 0));
+}
+
+// Two floats to E2M1, round to nearest even, `lo` in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+      "cvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two E2M1 codes (low nibble first) to two floats.
+__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.u8.u32 t, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+      : "=r"(h)
+      : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 8 elements of a block that four neighbouring lanes share -> 8 codes and the scale byte.
+__device__ __forceinline__ uint32_t mx4_quantize8(const float (&v)[8], uint32_t& scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  if (m >= 0x7F800000u) {   // an infinity or a NaN in the block
+    scale = 255;
+    return 0;
+  }
+  const int X = mx4_exponent(m);
+  scale = static_cast<uint32_t>(X + 127);
+  const float inv = exp2_int(-X);
+  uint32_t q = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+  return q;
+}
+
+// x [nblk, 32] -> codes [nblk, 16 B], scales [nblk]: rows of any width are runs of blocks.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const T* __restrict__ x, int64_t nblk,
+                                                             uint32_t* __restrict__ codes,
+                                                             uint8_t* __restrict__ scales) {
+  pdl_enter();
+  const int64_t total = nblk * 4;   // lanes; whole warps take part in the shuffles
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < total; i += step) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (i < total) load8<T>(x + i * 8, v);
+    uint32_t s;
+    const uint32_t q = mx4_quantize8(v, s);
+    if (i < total) {
+      codes[i] = q;
+      if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(s);
+    }
+  }
+}
+
+// Row-group table of a kernel: goff[g] (clamped into [0, rows]) and the prefix of 128-row
+// blocks per group.  Called by one whole warp; G <= kMaxGroups.
+__device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int rows, int* goff, int* blk) {
+  const int lane = threadIdx.x & 31;
+  int bad = 0;
+  for (int g = lane; g <= G; g += 32) {
+    int v = off == nullptr ? (g == 0 ? 0 : rows) : off[g];
+    if (v < 0 || v > rows) { bad = 1; v = min(max(v, 0), rows); }
+    goff[g] = v;
+  }
+  __syncwarp();
+  int running = 0;
+  if (lane == 0) blk[0] = 0;
+  for (int base = 0; base < G; base += 32) {
+    const int g = base + lane;
+    int cnt = 0;
+    if (g < G) {
+      const int n = goff[g + 1] - goff[g];
+      if (n < 0) bad = 1;
+      cnt = n > 0 ? (n + kBM - 1) / kBM : 0;
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (g < G) blk[g + 1] = running + incl;
+    running += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(DEVERR_BOUNDS);
+}
+
+// x [rows, K] bf16, rows grouped by off (null: one group) -> codes [rows, K/2] and scale
+// tiles, the row blocks counted group after group.  Rows outside every group are skipped.
+__global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, int rows, int K,
+                                                              const int32_t* __restrict__ off, int G, int max_blocks,
+                                                              uint32_t* __restrict__ codes,
+                                                              uint8_t* __restrict__ tiles) {
+  pdl_enter();
+  __shared__ int goff[kMaxGroups + 2];
+  __shared__ int blk[kMaxGroups + 2];
+  if (threadIdx.x < 32) mx4_group_table(off, G, rows, goff, blk);
+  __syncthreads();
+  const int nb = K / 32, kc = mx4_chunks(K);
+  const int64_t total = static_cast<int64_t>(rows) * nb * 4;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < total; i += step) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (i < total) load8<__nv_bfloat16>(x + i * 8, v);
+    uint32_t s;
+    const uint32_t q = mx4_quantize8(v, s);
+    if (i >= total) continue;
+    const int64_t b = i >> 2;
+    const int row = static_cast<int>(b / nb);
+    const int kb = static_cast<int>(b - static_cast<int64_t>(row) * nb);
+    codes[i] = q;
+    if ((i & 3) != 0) continue;
+    int lo = 0, hi = G;   // goff[lo] <= row < goff[hi] where the row is in a group
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (goff[mid] <= row) lo = mid; else hi = mid;
+    }
+    if (row < goff[lo] || row >= goff[lo + 1]) continue;
+    const int p = row - goff[lo];
+    const int rb = blk[lo] + p / kBM;
+    if (rb >= max_blocks) continue;   // offsets that are not ascending (flagged)
+    uint8_t* t = tiles + (static_cast<size_t>(rb) * kc) * 512 + 16 * (p & 31) + 4 * ((p & 127) >> 5);
+    t[static_cast<size_t>(kb >> 2) * 512 + (kb & 3)] = static_cast<uint8_t>(s);
+    if (kb == nb - 1)
+      for (int c = nb; c < 4 * kc; ++c) t[static_cast<size_t>(c >> 2) * 512 + (c & 3)] = 127;
+  }
+}
+
+// Scales [G, N, nb] as tiles, every group's row blocks on their own.  One thread per 4-byte
+// word (four K blocks of one row).
+__global__ void __launch_bounds__(256) mx4_scale_tiles_kernel(const uint8_t* __restrict__ scales, int G, int N,
+                                                              int nb, uint32_t* __restrict__ tiles) {
+  pdl_enter();
+  const int kc = 2 * ((nb + 7) / 8), nblk = (N + kBM - 1) / kBM;
+  const int64_t total = static_cast<int64_t>(G) * nblk * kc * 128;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const int w = static_cast<int>(i & 127);                 // word of the chunk: lane w / 4, row quarter w % 4
+    const int64_t chunk = i >> 7;
+    const int c = static_cast<int>(chunk % kc);
+    const int64_t rbg = chunk / kc;
+    const int rb = static_cast<int>(rbg % nblk);
+    const int g = static_cast<int>(rbg / nblk);
+    const int row = rb * kBM + (w & 3) * 32 + (w >> 2);
+    uint32_t v = 0x7F7F7F7Fu;
+    if (row < N) {
+      const uint8_t* s = scales + (static_cast<size_t>(g) * N + row) * nb;
+      v = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v |= (4 * c + b < nb ? static_cast<uint32_t>(s[4 * c + b]) : 127u) << (8 * b);
+    }
+    tiles[i] = v;
+  }
+}
+
+// codes [nblk, 16 B], scales [nblk] -> values; scale byte 255 gives NaN.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* __restrict__ codes,
+                                                               const uint8_t* __restrict__ scales, int64_t nblk,
+                                                               T* __restrict__ out) {
+  pdl_enter();
+  const int64_t total = nblk * 4;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const uint32_t q = codes[i];
+    const int s = scales[i >> 2];
+    const float f = s == 255 ? __uint_as_float(0x7FC00000u) : exp2_int(s - 127);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = e2m1x2_to_f32((q >> (8 * j)) & 0xFFu);
+      v[2 * j] = p.x * f;
+      v[2 * j + 1] = p.y * f;
+    }
+    store8<T>(out + i * 8, v);
+  }
+}
+
+static int mx4_blocks(const Launch& L, int64_t threads) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((threads + 255) / 256, int64_t(L.num_sms) * 8)));
+}
+
+cudaError_t mx4_quant_rows(const Launch& L, bool bf16, int64_t rows, int K, const void* x, uint8_t* codes,
+                           uint8_t* scales) {
+  const int64_t nblk = rows * (K / 32);
+  const int blocks = mx4_blocks(L, nblk * 4);
+  if (bf16)
+    pdl_launch(mx4_quant_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, L.stream,
+               static_cast<const __nv_bfloat16*>(x), nblk, reinterpret_cast<uint32_t*>(codes), scales);
+  else
+    pdl_launch(mx4_quant_rows_kernel<float>, dim3(blocks), dim3(256), 0, L.stream, static_cast<const float*>(x), nblk,
+               reinterpret_cast<uint32_t*>(codes), scales);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t mx4_dequant_rows(const Launch& L, bool bf16, int64_t rows, int K, const uint8_t* codes,
+                             const uint8_t* scales, void* out) {
+  const int64_t nblk = rows * (K / 32);
+  const int blocks = mx4_blocks(L, nblk * 4);
+  if (bf16)
+    pdl_launch(mx4_dequant_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, L.stream,
+               reinterpret_cast<const uint32_t*>(codes), scales, nblk, static_cast<__nv_bfloat16*>(out));
+  else
+    pdl_launch(mx4_dequant_rows_kernel<float>, dim3(blocks), dim3(256), 0, L.stream,
+               reinterpret_cast<const uint32_t*>(codes), scales, nblk, static_cast<float*>(out));
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t mx4_scale_tiles(const Launch& L, int G, int N, int K, const uint8_t* scales, uint8_t* tiles) {
+  const int64_t words = static_cast<int64_t>(G) * ((N + kBM - 1) / kBM) * mx4_chunks(K) * 128;
+  pdl_launch(mx4_scale_tiles_kernel, dim3(mx4_blocks(L, words)), dim3(256), 0, L.stream, scales, G, N, K / 32,
+             reinterpret_cast<uint32_t*>(tiles));
+  count_launch();
+  return cudaGetLastError();
+}
+
+// Row blocks that R rows in G groups can take: every group may end in a partial one.
+int64_t mx4_row_blocks(int64_t R, int G) { return (R + kBM - 1) / kBM + std::min<int64_t>(G - 1, R); }
+
+cudaError_t mx4_quant_tiles(const Launch& L, int64_t R, int K, const void* x, const int32_t* off, int G,
+                            uint8_t* codes, uint8_t* tiles) {
+  pdl_launch(mx4_quant_tiles_kernel, dim3(mx4_blocks(L, R * (K / 8))), dim3(256), 0, L.stream,
+             static_cast<const __nv_bfloat16*>(x), static_cast<int>(R), K, off, G,
+             static_cast<int>(mx4_row_blocks(R, G)), reinterpret_cast<uint32_t*>(codes), tiles);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,284 @@
+#pragma once
+// Host side of the MXFP4 product and of the expert block's training pass: tensor maps and
+// launches (tensor maps as in gemm_launch.cuh: boxes of 128 bytes x rows, 128-byte swizzle,
+// zeros out of range).
+#include "ffn_backward.cuh"
+#include "gemm_launch.cuh"
+#include "grouped_gemm_mx4.cuh"
+
+namespace moe {
+
+// Sets the kernel's dynamic shared memory once per device.
+template <auto kern>
+static cudaError_t allow_smem(int smem) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static std::mutex mu;
+  static uint64_t configured = 0;   // one bit per device
+  std::lock_guard<std::mutex> g(mu);
+  if (dev < 64 && ((configured >> dev) & 1u)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev < 64) configured |= uint64_t(1) << dev;
+  return e;
+}
+
+// Rows of bytes [groups, rows, row_bytes]; boxes of 128 B x box_rows, 128-byte swizzle.
+static cudaError_t make_tmap_bytes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows,
+                                   uint64_t groups, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {row_bytes, rows, groups ? groups : 1};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+  const cuuint32_t box[3] = {128, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups ? 3 : 2, const_cast<void*>(ptr), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// bf16 rows [rows, cols] that lie ld elements apart; boxes of 64 elements x 64 rows.
+static cudaError_t make_tmap_rows(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, 64};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// MXFP4 product
+// ---------------------------------------------------------------------------
+template <typename OutT>
+static cudaError_t launch_mx4(const Launch& L, const CUtensorMap& a, const CUtensorMap& b, const Mx4Args& args,
+                              int64_t max_tiles) {
+  auto kern = grouped_gemm_mx4_kernel<OutT>;
+  const cudaError_t e = allow_smem<grouped_gemm_mx4_kernel<OutT>>(Mx4Layout::SMEM);
+  if (e != cudaSuccess) return e;
+  pdl_launch(kern, dim3(static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms))), dim3(kGemmThreads),
+             Mx4Layout::SMEM, L.stream, a, b, args);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const uint8_t* codes, const uint8_t* tiles,
+                        const int32_t* off, const uint8_t* w_codes, const uint8_t* w_tiles, const void* bias,
+                        bool out_f32, void* out) {
+  CUtensorMap ta, tb;
+  cudaError_t e;
+  if ((e = make_tmap_bytes(&ta, codes, K / 2, R, 0, kBM)) != cudaSuccess) return e;
+  if ((e = make_tmap_bytes(&tb, w_codes, K / 2, N, G, kMx4TN)) != cudaSuccess) return e;
+  Mx4Args a{};
+  a.group_off = off;
+  a.num_groups = G;
+  a.m_total = static_cast<int>(R);
+  a.n_out = N;
+  a.k_dim = K;
+  a.tiles_a = tiles;
+  a.row_blocks = static_cast<int>(mx4_row_blocks(R, G));
+  a.tiles_w = w_tiles;
+  a.bias = static_cast<const __nv_bfloat16*>(bias);
+  a.out = out;
+  a.wait_limit_ns = L.wait_limit_ns;
+  const int64_t max_tiles = mx4_row_blocks(R, G) * ((N + kMx4TN - 1) / kMx4TN);
+  return out_f32 ? launch_mx4<float>(L, ta, tb, a, max_tiles) : launch_mx4<__nv_bfloat16>(L, ta, tb, a, max_tiles);
+}
+
+// ---------------------------------------------------------------------------
+// expert block, training pass
+// ---------------------------------------------------------------------------
+cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
+                               const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
+                               void* h) {
+  GemmArgs a = base_args(L);
+  a.group_off = expert_off;
+  a.num_groups = E;
+  a.m_total = static_cast<int>(R);
+  a.n_out = F;
+  a.k_dim = D;
+  a.bias0 = w.b_gate;
+  a.bias1 = w.b_up;
+  a.limit = act.limit;
+  a.alpha = act.alpha;
+  a.gate_lo = act.gate_lo;
+  a.out = h;
+  a.ldo = F;
+  a.gu = gu;
+  if (!bf16) {
+    const dim3 grid((F + kSimtBN - 1) / kSimtBN, static_cast<unsigned>((R + kSimtBM - 1) / kSimtBM + E));
+    pdl_launch(simt_grouped_gemm_f32<EPI_SWIGLU_SAVE>, dim3(grid), dim3(256), 0, L.stream,
+               static_cast<const float*>(x_perm), static_cast<const float*>(w.w_gate),
+               static_cast<const float*>(w.w_up), a);
+    count_launch();
+    return cudaGetLastError();
+  }
+  CUtensorMap ta, tg, tu;
+  cudaError_t e;
+  if ((e = make_tmap(&ta, x_perm, false, D, R, 0, kBM)) != cudaSuccess) return e;
+  if ((e = make_tmap(&tg, w.w_gate, false, D, F, E, kTNGateUp)) != cudaSuccess) return e;
+  if ((e = make_tmap(&tu, w.w_up, false, D, F, E, kTNGateUp)) != cudaSuccess) return e;
+  const int64_t tiles = max_row_blocks(R, E) * ((F + kTNGateUp - 1) / kTNGateUp);
+  return launch<__nv_bfloat16, kTNGateUp, 2, EPI_SWIGLU_SAVE, kStages>(L, ta, tg, tu, a, tiles);
+}
+
+template <int KIND, typename OutT>
+static cudaError_t launch_backward(const Launch& L, const BwdArgs<KIND>& args, int64_t max_tiles) {
+  auto kern = ffn_backward_kernel<KIND, OutT>;
+  const cudaError_t e = allow_smem<ffn_backward_kernel<KIND, OutT>>(BwdLayout::SMEM);
+  if (e != cudaSuccess) return e;
+  pdl_launch(kern, dim3(static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms))), dim3(kGemmThreads),
+             BwdLayout::SMEM, L.stream, args);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <int KIND>
+static BwdArgs<KIND> backward_args(const Launch& L, int64_t R, int E, int k_dim, const int32_t* off,
+                                   const Activation& act) {
+  BwdArgs<KIND> a{};
+  a.num_jobs = 1;
+  a.group_off = off;
+  a.num_groups = E;
+  a.m_total = static_cast<int>(R);
+  a.k_dim = k_dim;
+  a.limit = act.limit;
+  a.alpha = act.alpha;
+  a.gate_lo = act.gate_lo;
+  a.wait_limit_ns = L.wait_limit_ns;
+  return a;
+}
+
+static int64_t column_blocks(int n) { return (n + bwd_tile_n(n) - 1) / bwd_tile_n(n); }
+
+static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
+                                        const int32_t* off, const ExpertWeights& w, const Activation& act,
+                                        const void* gu, const void* h, const void* dy, void* dgu, void* dx,
+                                        const ExpertGrads& gr, bool grad_f32) {
+  cudaError_t e;
+  __nv_bfloat16* dg = static_cast<__nv_bfloat16*>(dgu);
+  if (dx != nullptr || gr.w_gate != nullptr || gr.w_up != nullptr) {
+    BwdArgs<BWD_DH> a = backward_args<BWD_DH>(L, R, E, D, off, act);
+    BwdJob& j = a.job[0];
+    if ((e = make_tmap(&j.a, dy, false, D, R, 0, kBM)) != cudaSuccess) return e;
+    if ((e = make_tmap(&j.b0, w.w_down, false, F, D, E, kBwdBK)) != cudaSuccess) return e;
+    j.out = dgu;
+    j.n = F;
+    a.gu = static_cast<const __nv_bfloat16*>(gu);
+    if ((e = launch_backward<BWD_DH, __nv_bfloat16>(L, a, max_row_blocks(R, E) * column_blocks(F))) != cudaSuccess)
+      return e;
+  }
+  if (dx != nullptr) {
+    BwdArgs<BWD_DX> a = backward_args<BWD_DX>(L, R, E, F, off, act);
+    BwdJob& j = a.job[0];
+    if ((e = make_tmap_halves(&j.a, dgu, F, R, kBM)) != cudaSuccess) return e;
+    if ((e = make_tmap(&j.b0, w.w_gate, false, D, F, E, kBwdBK)) != cudaSuccess) return e;
+    if ((e = make_tmap(&j.b1, w.w_up, false, D, F, E, kBwdBK)) != cudaSuccess) return e;
+    j.out = dx;
+    j.n = D;
+    if ((e = launch_backward<BWD_DX, __nv_bfloat16>(L, a, max_row_blocks(R, E) * column_blocks(D))) != cudaSuccess)
+      return e;
+  }
+  BwdArgs<BWD_DW> a = backward_args<BWD_DW>(L, R, E, 0, off, act);
+  a.num_jobs = 0;
+  int64_t tiles = 0;
+  auto add = [&](void* out, void* bias_out, const void* pa, int m, int64_t lda, const void* pb, int n) {
+    if (out == nullptr) return cudaSuccess;
+    BwdJob& j = a.job[a.num_jobs++];
+    j.out = out;
+    j.bias_out = bias_out;
+    j.m = m;
+    j.n = n;
+    tiles += int64_t(E) * ((m + kBM - 1) / kBM) * column_blocks(n);
+    const cudaError_t r = make_tmap_rows(&j.a, pa, m, R, lda);
+    return r != cudaSuccess ? r : make_tmap_rows(&j.b0, pb, n, R, n);
+  };
+  if ((e = add(gr.w_down, gr.b_down, dy, D, D, h, F)) != cudaSuccess) return e;
+  if ((e = add(gr.w_gate, gr.b_gate, dg, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
+  if ((e = add(gr.w_up, gr.b_up, dg + F, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
+  if (a.num_jobs == 0) return cudaSuccess;
+  return grad_f32 ? launch_backward<BWD_DW, float>(L, a, tiles) : launch_backward<BWD_DW, __nv_bfloat16>(L, a, tiles);
+}
+
+static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
+                                       const int32_t* off, const ExpertWeights& w, const Activation& act,
+                                       const void* gu, const void* h, const void* dy, void* dgu, void* dx,
+                                       const ExpertGrads& gr) {
+  SimtBwdArgs p{};
+  p.group_off = off;
+  p.num_groups = E;
+  p.m_total = static_cast<int>(R);
+  p.limit = act.limit;
+  p.alpha = act.alpha;
+  p.gate_lo = act.gate_lo;
+  const unsigned row_tiles = static_cast<unsigned>((R + kSimtBM - 1) / kSimtBM + E);
+  auto col_tiles = [](int n) { return static_cast<unsigned>((n + kSimtBN - 1) / kSimtBN); };
+  if (dx != nullptr || gr.w_gate != nullptr || gr.w_up != nullptr) {
+    p.n = F;
+    p.k = D;
+    p.a = static_cast<const float*>(dy);
+    p.b0 = static_cast<const float*>(w.w_down);
+    p.gu = static_cast<const float*>(gu);
+    p.out = static_cast<float*>(dgu);
+    pdl_launch(simt_backward_kernel<BWD_DH>, dim3(col_tiles(F), row_tiles), dim3(256), 0, L.stream, p);
+    count_launch();
+  }
+  if (dx != nullptr) {
+    p.n = D;
+    p.k = F;
+    p.a = static_cast<const float*>(dgu);
+    p.b0 = static_cast<const float*>(w.w_gate);
+    p.b1 = static_cast<const float*>(w.w_up);
+    p.out = static_cast<float*>(dx);
+    pdl_launch(simt_backward_kernel<BWD_DX>, dim3(col_tiles(D), row_tiles), dim3(256), 0, L.stream, p);
+    count_launch();
+  }
+  auto grad = [&](void* out, void* bias_out, const void* pa, int m, int lda, const void* pb, int n) {
+    if (out == nullptr) return;
+    p.out = static_cast<float*>(out);
+    p.bias_out = static_cast<float*>(bias_out);
+    p.a = static_cast<const float*>(pa);
+    p.b0 = static_cast<const float*>(pb);
+    p.m = m;
+    p.n = n;
+    p.lda = lda;
+    p.ldb = n;
+    pdl_launch(simt_backward_kernel<BWD_DW>, dim3(col_tiles(n), static_cast<unsigned>((m + kSimtBM - 1) / kSimtBM), E),
+               dim3(256), 0, L.stream, p);
+    count_launch();
+  };
+  grad(gr.w_down, gr.b_down, dy, D, D, h, F);
+  grad(gr.w_gate, gr.b_gate, dgu, F, 2 * F, x_perm, D);
+  grad(gr.w_up, gr.b_up, static_cast<float*>(dgu) + F, F, 2 * F, x_perm, D);
+  return cudaGetLastError();
+}
+
+cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
+                            const int32_t* expert_off, const ExpertWeights& w, const Activation& act, const void* gu,
+                            const void* h, const void* dy, void* dgu, void* dx, const ExpertGrads& grads,
+                            bool grad_f32) {
+  if (bf16)
+    return expert_backward_bf16(L, R, D, F, E, x_perm, expert_off, w, act, gu, h, dy, dgu, dx, grads, grad_f32);
+  return expert_backward_f32(L, R, D, F, E, x_perm, expert_off, w, act, gu, h, dy, dgu, dx, grads);
+}
+
+cudaError_t combine_backward(const Launch& L, bool bf16, int64_t T, int D, int k, const void* dy, const void* y_perm,
+                             const int32_t* row_of_slot, const float* w, void* dy_perm, float* dw) {
+  const dim3 grid(static_cast<unsigned>(T)), block(kCombineBwdThreads);
+  if (bf16)
+    pdl_launch(combine_backward_kernel<__nv_bfloat16>, grid, block, 0, L.stream,
+               static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(y_perm), row_of_slot, w,
+               static_cast<int>(T), k, D, static_cast<__nv_bfloat16*>(dy_perm), dw);
+  else
+    pdl_launch(combine_backward_kernel<float>, grid, block, 0, L.stream, static_cast<const float*>(dy),
+               static_cast<const float*>(y_perm), row_of_slot, w, static_cast<int>(T), k, D,
+               static_cast<float*>(dy_perm), dw);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace moe
