@@ -21,15 +21,17 @@
 // operands, before the MMA reads them (zeroing one would let an infinity or a NaN of a
 // neighbouring expert through as 0 * inf).
 //
-// Bias gradients: for the tiles of the first column block the issuer adds one N = 16 MMA a
-// step whose B operand is a tile of ones, into the 16 TMEM columns that the <= 240-column
-// tile leaves free: the sums cost no further pass over dy and dgu.
+// Bias gradients: for the tiles of the first column block, which DW keeps at most 192
+// columns wide, the issuer adds one N = 16 MMA a step whose B operand is a tile of ones, into
+// TMEM columns that the tile leaves free: the sums cost no further pass over dy and dgu.
 //
 // dg and du are rounded to bf16 between DH and the two products that read them (they are
 // tensor-core operands); all sums are fp32.
 //
-// Tile 128 x tn, tn = the columns split evenly into blocks of at most 240 (a multiple of
-// 16; 2880 = 12 x 240), four 64-deep stages, two accumulator buffers; roles as in
+// Tile 128 x (64 to 256 columns): the columns are split into blocks of 1 to 4 boxes of 64,
+// as even as that allows (2880 = 3 x 192 + 9 x 256), so that every box row is one 128-byte
+// line of L2 -- evener blocks of 240 columns start between lines, and each box row then
+// takes two L2 requests.  Four 64-deep stages, two accumulator buffers; roles as in
 // grouped_gemm.cuh.  DH and DX walk (expert, row block, column block) tiles of the ragged
 // rows, DW walks (matrix, expert, 128-row block, column block) tiles of the gradients.
 #pragma once
@@ -40,27 +42,41 @@ namespace moe {
 
 enum BwdKind : int { BWD_DH = 0, BWD_DX = 1, BWD_DW = 2 };
 
-constexpr int kBwdTN = 240;          // most columns of a tile
 constexpr int kBwdBK = 64;           // K per stage
 constexpr int kBwdStages = 4;
 constexpr int kBwdBox = 64 * 128;    // bytes of a [64 K-rows x 64 elements] box
-constexpr int kBwdOnesCol = 240;     // TMEM column of the bias sums inside an accumulator buffer
+constexpr int kBwdOnesCol = 192;     // TMEM column of the bias sums inside an accumulator buffer
 
+constexpr int kBwdThreads = 384;
+constexpr int kBwdEpiWarps = 8;
+constexpr int kBwdSched = 4;         // tiles the scheduler is ahead
+
+template <int KIND>
 struct BwdLayout {
   static constexpr int A_BYTES = 2 * kBwdBox;
   static constexpr int B_BYTES = 4 * kBwdBox;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int ONES = 2048;               // 16 rows x 128 B of bf16 ones
-  static constexpr int STAGING = 4 * 32 * 144;
-  static constexpr int EXTRA = 1024 + 4096;
+  static constexpr int ONES = KIND == BWD_DW ? 2048 : 0;                     // 16 rows x 128 B of bf16 ones
+  // epilogue staging of a warp: 32 rows of 64 B + 16 B;  DH: of g and u, 32 B + 16 B each
+  static constexpr int STAGING_WARP = KIND == BWD_DH ? 2 * 32 * 48 : 32 * 80;
+  static constexpr int STAGING = kBwdEpiWarps * STAGING_WARP;
+  static constexpr int EXTRA = 1024 + 3072;
   static constexpr int SMEM = kBwdStages * STAGE_BYTES + ONES + STAGING + EXTRA;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-// Columns per tile: N split evenly into blocks of at most 240, in steps of 16.
-__host__ __device__ constexpr int bwd_tile_n(int N) {
-  const int blocks = (N + kBwdTN - 1) / kBwdTN;
-  return ((N + blocks - 1) / blocks + 15) / 16 * 16;
+// Column blocks of N columns: 1 to 4 boxes of 64 each (3 at most for the first one if
+// `spare`), differing by at most one box, the narrower ones first.
+__host__ __device__ constexpr int bwd_col_blocks(int N, bool spare) {
+  return ((N + 63) / 64 + (spare ? 1 : 0) + 3) / 4;
+}
+struct BwdCols {
+  int first, boxes;   // first column, number of 64-column boxes
+};
+__host__ __device__ inline BwdCols bwd_cols(int N, int blocks, int j) {
+  const int n64 = (N + 63) / 64;
+  const int q = n64 / blocks, narrow = blocks - n64 % blocks;
+  return BwdCols{64 * (j * q + (j > narrow ? j - narrow : 0)), q + (j >= narrow ? 1 : 0)};
 }
 
 // One product of a launch.  DH: A = dy, B0 = Wd.  DX: A = dgu (halves), B0 = Wg, B1 = Wu.
@@ -70,6 +86,7 @@ struct BwdJob {
   void* out;
   void* bias_out;   // DW: [G, m] column sums of A, or null
   int m, n;         // DW: rows and columns of the gradient;  DH, DX: n = columns of the output
+  int nt;           // column blocks
 };
 
 template <int KIND>
@@ -108,75 +125,121 @@ __device__ __forceinline__ void act_grad(float dh, float g, float u, float limit
 }
 
 struct BwdTile {
-  int job, g, m0, m_end, n0;   // DW: m0 / n0 inside the gradient;  DH, DX: m0 a row of A
+  int job, g;           // job -1: no more tiles
+  int m0, m_end;        // DW: rows of the gradient;  DH, DX: rows of A
+  int n0, boxes;        // first column, 64-column boxes
+  int kb;               // 64-deep K blocks
+  int r0, rows;         // DW: the expert's rows
 };
 
 template <int KIND>
 __device__ __forceinline__ BwdTile bwd_tile(int i, const int* tile_off, const int* goff, const BwdArgs<KIND>& a) {
   BwdTile t;
+  t.job = 0;
+  int nb;
   if constexpr (KIND == BWD_DW) {
-    t.job = 0;
-    int mt = 0, nt = 0;
+    int mt = 0;
     for (;; ++t.job) {
       mt = (a.job[t.job].m + kBM - 1) / kBM;
-      nt = (a.job[t.job].n + bwd_tile_n(a.job[t.job].n) - 1) / bwd_tile_n(a.job[t.job].n);
-      const int n = a.num_groups * mt * nt;
+      const int n = a.num_groups * mt * a.job[t.job].nt;
       if (i < n || t.job + 1 == a.num_jobs) break;
       i -= n;
     }
+    const int nt = a.job[t.job].nt;
     t.g = i / (mt * nt);
     i -= t.g * mt * nt;
     // bands of kGroupBand row blocks, the row block fastest: neighbours share operand rows in L2
     const int band = i / (kGroupBand * nt);
     const int rem = i - band * kGroupBand * nt;
     const int rows = min(kGroupBand, mt - band * kGroupBand);
-    t.n0 = (rem / rows) * bwd_tile_n(a.job[t.job].n);
-    t.m0 = (band * kGroupBand + rem % rows) * kBM;
+    nb = rem / rows;
+    t.m0 = (band * kGroupBand + rem - nb * rows) * kBM;
     t.m_end = a.job[t.job].m;
   } else {
-    const int tn = bwd_tile_n(a.job[0].n);
-    const TileInfo ti = decode_tile(i, tile_off, goff, a.num_groups, (a.job[0].n + tn - 1) / tn, tn);
-    t.job = 0;
+    const TileInfo ti = decode_tile(i, tile_off, goff, a.num_groups, a.job[0].nt, 1);
     t.g = ti.g;
     t.m0 = ti.m0;
     t.m_end = ti.m_end;
-    t.n0 = ti.n0;
+    nb = ti.n0;
   }
+  const BwdCols c = bwd_cols(a.job[t.job].n, a.job[t.job].nt, nb);
+  t.n0 = c.first;
+  t.boxes = c.boxes;
   return t;
 }
 
+// 32 rows x 64 bytes that the warp's lanes hold (lane = row, v its columns) to global rows
+// through the warp's staging area: a store instruction covers eight 64-byte runs of rows.
+template <typename T>
+__device__ __forceinline__ void store_rows64(uint8_t* stage, T* out, size_t ldo, int rows, int cols, const float* v) {
+  constexpr int PER = 16 / static_cast<int>(sizeof(T));   // columns per 16-byte piece
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    uint4 u;
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[p * PER + 2 * j], v[p * PER + 2 * j + 1]);
+    } else {
+      u = make_uint4(__float_as_uint(v[p * PER]), __float_as_uint(v[p * PER + 1]), __float_as_uint(v[p * PER + 2]),
+                     __float_as_uint(v[p * PER + 3]));
+    }
+    *reinterpret_cast<uint4*>(stage + lane * 80 + p * 16) = u;
+  }
+  __syncwarp();
+  const int piece = lane & 3;
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 8 + (lane >> 2);
+    if (r < rows && piece * PER < cols)
+      *reinterpret_cast<uint4*>(out + r * ldo + piece * PER) = *reinterpret_cast<const uint4*>(stage + r * 80 + piece * 16);
+  }
+}
+
 template <int KIND, typename OutT>
-__global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __grid_constant__ BwdArgs<KIND> args) {
+__global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __grid_constant__ BwdArgs<KIND> args) {
   pdl_enter();
-  using LY = BwdLayout;
+  using LY = BwdLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ones = smem + kBwdStages * LY::STAGE_BYTES;
   uint8_t* staging = ones + LY::ONES;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + LY::STAGING);
-  uint64_t* empty = full + kBwdStages;
+  uint64_t* ready = full + kBwdStages;          // DW: the blanker has seen the stage
+  uint64_t* empty = ready + kBwdStages;
   uint64_t* tfull = empty + kBwdStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* sfull = tempty + 2;                 // scheduler ring
+  uint64_t* sempty = sfull + kBwdSched;
+  uint64_t* drain = sempty + kBwdSched;
+  BwdTile* ring = reinterpret_cast<BwdTile*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kBwdSched);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* never_flag = abort_flag + 1;
-  int* tile_off = never_flag + 2;              // [G+1]
-  int* goff = tile_off + (kMaxGroups + 2);     // [G+1]
+  int* tile_off = never_flag + 1;              // [G+1]
+  int* goff = tile_off + (kMaxGroups + 1);     // [G+1]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = args.num_groups;
   const uint64_t lim = args.wait_limit_ns;
+  constexpr int kConsumers = 2 + kBwdEpiWarps + (KIND == BWD_DW ? 1 : 0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kBwdStages; ++s) {
       mbar_init(&full[s], 1);
+      mbar_init(&ready[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 128);
+      mbar_init(&tempty[b], 32 * kBwdEpiWarps);
+    }
+    for (int q = 0; q < kBwdSched; ++q) {
+      mbar_init(&sfull[q], 1);
+      mbar_init(&sempty[q], kConsumers);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -194,7 +257,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __g
   } else if (warp == 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
-  } else if (KIND == BWD_DW) {
+  } else if (KIND == BWD_DW && warp < 6) {
     for (int i = threadIdx.x - 64; i < LY::ONES / 4; i += 128) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
   }
@@ -202,48 +265,77 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  int total = 0;
-  if constexpr (KIND == BWD_DW) {
-    for (int j = 0; j < args.num_jobs; ++j) {
-      const int tn = bwd_tile_n(args.job[j].n);
-      total += G * ((args.job[j].m + kBM - 1) / kBM) * ((args.job[j].n + tn - 1) / tn);
-    }
-  } else {
-    const int tn = bwd_tile_n(args.job[0].n);
-    total = tile_off[G] * ((args.job[0].n + tn - 1) / tn);
-  }
-  // 64-deep K blocks of a tile (DW: of its expert's rows; DX: of both halves)
-  const int KB1 = (args.k_dim + kBwdBK - 1) / kBwdBK;
-  auto k_blocks = [&](const BwdTile& t) {
-    if (KIND == BWD_DW) return max(0, goff[t.g + 1] - goff[t.g] + kBwdBK - 1) / kBwdBK;
-    return KIND == BWD_DX ? 2 * KB1 : KB1;
-  };
+  const int KB1 = (args.k_dim + kBwdBK - 1) / kBwdBK;   // DH, DX: K blocks (of one half)
 
-  if (warp == 0) {
+  // The next tile from the scheduler's ring; false when a wait gave up.  One thread, or a
+  // whole warp (which then agrees on the answer).
+  auto next_tile = [&](int n, BwdTile& t, bool whole_warp) {
+    const int q = n % kBwdSched;
+    bool got = mbar_wait(&sfull[q], (n / kBwdSched) & 1, abort_flag, lim);
+    if (whole_warp) got = __all_sync(0xffffffffu, got);
+    if (!got) return false;
+    t = ring[q];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(&sempty[q]);
+    return true;
+  };
+  bool ok = true;
+
+  if (warp == 2 + kBwdEpiWarps) {
+    // ------------------------------------------------------------ scheduler
+    if (lane == 0) {
+      int total = 0;
+      if constexpr (KIND == BWD_DW) {
+        for (int j = 0; j < args.num_jobs; ++j) total += G * ((args.job[j].m + kBM - 1) / kBM) * args.job[j].nt;
+      } else {
+        total = tile_off[G] * args.job[0].nt;
+      }
+      int n = 0;
+      for (int i = blockIdx.x;; i += gridDim.x, ++n) {
+        BwdTile t;
+        t.job = -1;
+        if (i < total) {
+          t = bwd_tile<KIND>(i, tile_off, goff, args);
+          t.r0 = goff[t.g];
+          t.rows = max(0, goff[t.g + 1] - t.r0);
+          t.kb = KIND == BWD_DW ? (t.rows + kBwdBK - 1) / kBwdBK : KIND == BWD_DX ? 2 * KB1 : KB1;
+        }
+        const int q = n % kBwdSched;
+        if (!mbar_wait(&sempty[q], ((n / kBwdSched) & 1) ^ 1, abort_flag, lim)) { ok = false; break; }
+        ring[q] = t;
+        mbar_arrive(&sfull[q]);
+        if (i >= total) break;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(DEVERR_TIMEOUT);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
-        const BwdTile ti = bwd_tile<KIND>(i, tile_off, goff, args);
+      BwdTile ti;
+      for (int n = 0;; ++n) {
+        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (ti.job < 0) break;
         const BwdJob& jb = args.job[ti.job];
-        const int nbox = (bwd_tile_n(jb.n) + 63) / 64;
-        const int KB = k_blocks(ti);
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < ti.kb; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[s], LY::A_BYTES + nbox * kBwdBox);
+          mbar_arrive_expect_tx(&full[s], LY::A_BYTES + ti.boxes * kBwdBox);
           uint8_t* sa = smem + s * LY::STAGE_BYTES;
           uint8_t* sb = sa + LY::A_BYTES;
           if constexpr (KIND == BWD_DW) {
-            const int r = goff[ti.g] + kb * kBwdBK;
-            for (int q = 0; q < nbox; ++q) tma_load_2d(sb + q * kBwdBox, &jb.b0, &full[s], ti.n0 + 64 * q, r);
+            const int r = ti.r0 + kb * kBwdBK;
+            for (int q = 0; q < ti.boxes; ++q) tma_load_2d(sb + q * kBwdBox, &jb.b0, &full[s], ti.n0 + 64 * q, r);
             for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kBwdBox, &jb.a, &full[s], ti.m0 + 64 * q, r);
           } else {
             const int half = (KIND == BWD_DX && kb >= KB1) ? 1 : 0;
             const int k0 = (kb - half * KB1) * kBwdBK;
             const CUtensorMap* tb = half ? &jb.b1 : &jb.b0;
-            for (int q = 0; q < nbox; ++q) tma_load_3d(sb + q * kBwdBox, tb, &full[s], ti.n0 + 64 * q, k0, ti.g);
+            for (int q = 0; q < ti.boxes; ++q) tma_load_3d(sb + q * kBwdBox, tb, &full[s], ti.n0 + 64 * q, k0, ti.g);
             if (KIND == BWD_DX) tma_load_3d(sa, &jb.a, &full[s], k0, half, ti.m0);
             else tma_load_2d(sa, &jb.a, &full[s], k0, ti.m0);
           }
@@ -251,6 +343,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __g
           issued_par = (issued_par & ~(1u << s)) | (ph << s);
           if (++s == kBwdStages) { s = 0; ph ^= 1u; }
         }
+        if (!ok) break;
       }
       if (!ok) {
         *abort_flag = 1;
@@ -263,70 +356,51 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __g
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // Lane 0 waits and issues.  The whole warp takes part where a DW tile's last block has
-    // rows to blank; `ok` is lane 0's until the warp agrees on it at the end of a tile.
-    int s = 0, it = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; ok && i < total; i += gridDim.x, ++it) {
-      const BwdTile ti = bwd_tile<KIND>(i, tile_off, goff, args);
-      const BwdJob& jb = args.job[ti.job];
-      const int KB = k_blocks(ti);
-      const int tn = bwd_tile_n(jb.n);
-      const uint32_t idesc = make_idesc(kBM, tn, 1u) | (1u << 16) | (KIND == BWD_DW ? 1u << 15 : 0u);
-      const uint32_t idesc_ones = make_idesc(kBM, 16, 1u) | (1u << 15);
-      const bool sums = KIND == BWD_DW && ti.n0 == 0 && jb.bias_out != nullptr;
-      const int acc = it & 1;
-      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
-      if (lane == 0) {
-        ok = mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, abort_flag, lim);
-        tc_fence_after();
-      }
-      for (int kb = 0; kb < KB; ++kb) {
-        const uint32_t a_addr = smem_u32(smem + s * LY::STAGE_BYTES);
-        const uint32_t b_addr = a_addr + LY::A_BYTES;
-        int steps = kBwdBK / 16;
-        if (KIND == BWD_DW && kb == KB - 1) {
-          const int valid = goff[ti.g + 1] - goff[ti.g] - kb * kBwdBK;   // 1..64
-          steps = (valid + 15) / 16;
-          if ((valid & 15) != 0) {
-            const bool got = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, lim));
-            if (got) {
-              uint8_t* st = smem + s * LY::STAGE_BYTES;
-              const int nbox = 2 + (tn + 63) / 64;
-              const int blank = 16 * steps - valid;   // rows valid .. 16 steps - 1 of every box
-              for (int q = lane; q < nbox * blank * 8; q += 32) {
-                const int box = q / (blank * 8), rem = q - box * blank * 8;
-                *reinterpret_cast<uint4*>(st + box * kBwdBox + valid * 128 + rem * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-          }
-        }
-        if (lane == 0) {
-          if (ok) ok = mbar_wait(&full[s], ph, abort_flag, lim);
-          if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kBwdBK / 16; ++kk) {
-              if (kk < steps) {
-                const uint64_t ad = KIND == BWD_DW ? sw128_mnmajor_desc(a_addr + kk * 2048)
-                                                   : sw128_kmajor_desc(a_addr + kk * 32);
-                const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
-                tc_mma<false>(d_tmem, ad, sw128_mnmajor_desc(b_addr + kk * 2048), idesc, accumulate);
-                if (sums) tc_mma<false>(d_tmem + kBwdOnesCol, ad, sw128_kmajor_desc(smem_u32(ones)), idesc_ones, accumulate);
-              }
-            }
-            tc_commit(&empty[s]);
-          }
-        }
-        if (++s == kBwdStages) { s = 0; ph ^= 1u; }
-      }
-      if (lane == 0 && ok) tc_commit(&tfull[acc]);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    }
+    // One thread issues every MMA (128 cycles each at 256 columns): descriptors are made
+    // once and stepped by additions (built per MMA they took 264 cycles an MMA).
     if (lane == 0) {
+      const uint32_t s_addr = smem_u32(smem);
+      const uint64_t a_desc = KIND == BWD_DW ? sw128_mnmajor_desc(s_addr) : sw128_kmajor_desc(s_addr);
+      const uint64_t b_desc = sw128_mnmajor_desc(s_addr + LY::A_BYTES);
+      const uint64_t ones_desc = sw128_kmajor_desc(smem_u32(ones));
+      constexpr int kAStep = KIND == BWD_DW ? 2048 / 16 : 32 / 16;   // of 16 K elements
+      const uint32_t idesc_ones = make_idesc(kBM, 16, 1u) | (1u << 15);
+      uint64_t* loaded = KIND == BWD_DW ? ready : full;
+      int s = 0;
+      uint32_t ph = 0;
+      BwdTile ti;
+      for (int n = 0;; ++n) {
+        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (ti.job < 0) break;
+        const uint32_t idesc = make_idesc(kBM, 64 * ti.boxes, 1u) | (1u << 16) | (KIND == BWD_DW ? 1u << 15 : 0u);
+        const bool sums = KIND == BWD_DW && ti.n0 == 0 && args.job[ti.job].bias_out != nullptr;
+        const int acc = n & 1;
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
+        if (!mbar_wait(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        tc_fence_after();
+        for (int kb = 0; kb < ti.kb; ++kb) {
+          if (!mbar_wait(&loaded[s], ph, abort_flag, lim)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>(s * (LY::STAGE_BYTES >> 4));
+          const uint64_t ad = a_desc + so, bd = b_desc + so;
+          const int steps = KIND == BWD_DW ? min(kBwdBK / 16, (ti.rows - kb * kBwdBK + 15) / 16) : kBwdBK / 16;
+          if (steps == kBwdBK / 16 && !sums) {
+#pragma unroll
+            for (int kk = 0; kk < kBwdBK / 16; ++kk)
+              tc_mma<false>(d_tmem, ad + kk * kAStep, bd + kk * 128, idesc, (kb | kk) != 0 ? 1u : 0u);
+          } else {
+            for (int kk = 0; kk < steps; ++kk) {
+              const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
+              tc_mma<false>(d_tmem, ad + kk * kAStep, bd + kk * 128, idesc, accumulate);
+              if (sums) tc_mma<false>(d_tmem + kBwdOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
+            }
+          }
+          tc_commit(&empty[s]);
+          if (++s == kBwdStages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit(&tfull[acc]);
+      }
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
@@ -335,69 +409,109 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __g
       if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5)
-    constexpr int COLS = 128 / static_cast<int>(sizeof(OutT));
-    const int quarter = warp & 3;
-    uint8_t* stage = staging + quarter * (32 * 144);
-    int it = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; i < total; i += gridDim.x, ++it) {
-      const BwdTile ti = bwd_tile<KIND>(i, tile_off, goff, args);
+  } else if (warp < 2 + kBwdEpiWarps) {
+    // ------------------------------------------------------------ epilogue (warps 2..9)
+    // Two warps share a TMEM lane quarter and take its column chunks in turn.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stage = staging + (warp - 2) * LY::STAGING_WARP;
+    BwdTile ti;
+    for (int n = 0;; ++n) {
+      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (ti.job < 0) break;
       const BwdJob& jb = args.job[ti.job];
-      const int tn = bwd_tile_n(jb.n);
-      const int acc = it & 1;
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], (it >> 1) & 1, abort_flag, lim));
-      if (!got) { ok = false; break; }
-      tc_fence_after();
+      const int acc = n & 1;
+      const int row0 = ti.m0 + quarter * 32;
+      const int rows = ti.m_end - row0;
+      const int width = min(64 * ti.boxes, jb.n - ti.n0);
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kAccStride);
-      const int row0 = ti.m0 + quarter * 32;
-      const bool none = KIND == BWD_DW && goff[ti.g + 1] <= goff[ti.g];   // no rows: the gradient is zero
-      const int width = min(tn, jb.n - ti.n0);
       if constexpr (KIND == BWD_DH) {
+        // 16 columns at a time: g and u come in 32-byte runs of rows (the next chunk's while
+        // this one is computed, the first before the accumulator is complete), turn into row
+        // order through the staging area, and dg and du leave the same way
         const int F = jb.n;
-        const int row = row0 + lane;
-        const bool rvalid = row < ti.m_end;
-        const __nv_bfloat16* g = args.gu + static_cast<size_t>(rvalid ? row : 0) * 2 * F + ti.n0;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + static_cast<size_t>(row) * 2 * F + ti.n0;
-#pragma unroll 1
-        for (int c = 0; c < width; c += 8) {
-          float v[8];
-          tmem_ld8(tbase + c, v);
-          tmem_ld_wait();
-          if (rvalid) {
-            float gv[8], uv[8], dg[8], du[8];
-            load8<__nv_bfloat16>(g + c, gv);
-            load8<__nv_bfloat16>(g + F + c, uv);
+        const int r2 = lane >> 1, piece = lane & 1;
+        const __nv_bfloat16* gu = args.gu + static_cast<size_t>(row0) * 2 * F + ti.n0 + piece * 8;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + static_cast<size_t>(row0) * 2 * F + ti.n0 + piece * 8;
+        uint8_t* su = stage + 32 * 48;         // u's half of the warp's staging
+        uint4 pre[4];
+        auto fetch = [&](int c) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              act_grad(v[j], gv[j], uv[j], args.limit, args.alpha, args.gate_lo, dg[j], du[j]);
-            store8<__nv_bfloat16>(out + c, dg);
-            store8<__nv_bfloat16>(out + F + c, du);
+          for (int p = 0; p < 2; ++p) {
+            const int r = p * 16 + r2;
+            pre[p] = pre[2 + p] = make_uint4(0, 0, 0, 0);
+            if (c < width && r < rows) {
+              pre[p] = *reinterpret_cast<const uint4*>(gu + static_cast<size_t>(r) * 2 * F + c);
+              pre[2 + p] = *reinterpret_cast<const uint4*>(gu + static_cast<size_t>(r) * 2 * F + F + c);
+            }
+          }
+        };
+        fetch(16 * half);
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 16 * half; c < width; c += 32) {
+          __syncwarp();
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            *reinterpret_cast<uint4*>(stage + (p * 16 + r2) * 48 + piece * 16) = pre[p];
+            *reinterpret_cast<uint4*>(su + (p * 16 + r2) * 48 + piece * 16) = pre[2 + p];
+          }
+          __syncwarp();
+          fetch(c + 32);
+          float v[16];
+          tmem_ld8(tbase + c, *reinterpret_cast<float(*)[8]>(v));
+          tmem_ld8(tbase + c + 8, *reinterpret_cast<float(*)[8]>(v + 8));
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
+            float gv[8], uv[8], dg[8], du[8];
+            __nv_bfloat16* pg = reinterpret_cast<__nv_bfloat16*>(stage + lane * 48 + j * 2);
+            __nv_bfloat16* pu = reinterpret_cast<__nv_bfloat16*>(su + lane * 48 + j * 2);
+            load8<__nv_bfloat16>(pg, gv);
+            load8<__nv_bfloat16>(pu, uv);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              act_grad(v[j + q], gv[q], uv[q], args.limit, args.alpha, args.gate_lo, dg[q], du[q]);
+            store8<__nv_bfloat16>(pg, dg);
+            store8<__nv_bfloat16>(pu, du);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int r = p * 16 + r2;
+            if (r < rows) {
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * 2 * F + c) =
+                  *reinterpret_cast<const uint4*>(stage + r * 48 + piece * 16);
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * 2 * F + F + c) =
+                  *reinterpret_cast<const uint4*>(su + r * 48 + piece * 16);
+            }
           }
         }
       } else {
+        constexpr int COLS = 64 / static_cast<int>(sizeof(OutT));
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
+        tc_fence_after();
+        const bool none = KIND == BWD_DW && ti.rows == 0;   // the gradient is zero
         const size_t row_base = KIND == BWD_DW ? static_cast<size_t>(ti.g) * jb.m : 0;
         OutT* out = static_cast<OutT*>(jb.out) + (row_base + row0) * jb.n + ti.n0;
 #pragma unroll 1
-        for (int c = 0; c < width; c += COLS) {
+        for (int c = COLS * half; c < width; c += 2 * COLS) {
           float v[COLS];
 #pragma unroll
-          for (int j = 0; j < COLS; j += 8)
-            if (c + j < width) tmem_ld8(tbase + c + j, *reinterpret_cast<float(*)[8]>(v + j));
+          for (int j = 0; j < COLS; j += 8) tmem_ld8(tbase + c + j, *reinterpret_cast<float(*)[8]>(v + j));
           tmem_ld_wait();
           if (none) {
 #pragma unroll
             for (int j = 0; j < COLS; ++j) v[j] = 0.0f;
           }
-          store_rows_staged<OutT>(stage, out + c, jb.n, ti.m_end - row0, width - c, v);
+          store_rows64<OutT>(stage, out + c, jb.n, rows, width - c, v);
         }
-        if (KIND == BWD_DW && ti.n0 == 0 && jb.bias_out != nullptr) {
+        if (KIND == BWD_DW && half == 0 && ti.n0 == 0 && jb.bias_out != nullptr) {
           float b[8];
           tmem_ld8(tbase + kBwdOnesCol, b);
           tmem_ld_wait();
-          if (row0 + lane < ti.m_end) {
+          if (lane < rows) {
             const float sum = none ? 0.0f : b[0];
             OutT* bo = static_cast<OutT*>(jb.bias_out) + row_base + row0 + lane;
             if constexpr (sizeof(OutT) == 2) *bo = __float2bfloat16_rn(sum);
@@ -407,6 +521,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_backward_kernel(const __g
       }
       tc_fence_before();
       mbar_arrive(&tempty[acc]);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      flag_error(DEVERR_TIMEOUT);
+    }
+  } else if (KIND == BWD_DW) {
+    // ------------------------------------------------------------ blanker
+    // Passes every loaded stage on to the issuer, after blanking the rows between the end
+    // of the expert and the end of the last 16-row step.
+    int s = 0;
+    uint32_t ph = 0;
+    BwdTile ti;
+    for (int n = 0; ok; ++n) {
+      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (ti.job < 0) break;
+      for (int kb = 0; kb < ti.kb; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, lim))) { ok = false; break; }
+        const int valid = ti.rows - kb * kBwdBK;
+        if (valid < kBwdBK && (valid & 15) != 0) {
+          uint8_t* st = smem + s * LY::STAGE_BYTES + valid * 128;
+          const int pieces = (16 - (valid & 15)) * 8;
+          for (int box = 0; box < 2 + ti.boxes; ++box)
+            for (int q = lane; q < pieces; q += 32)
+              *reinterpret_cast<uint4*>(st + box * kBwdBox + q * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();   // read by the tensor core (async proxy)
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[s]);
+        if (++s == kBwdStages) { s = 0; ph ^= 1u; }
+      }
     }
     if (!ok) {
       *abort_flag = 1;

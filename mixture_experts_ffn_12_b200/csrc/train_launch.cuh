@@ -129,10 +129,10 @@ cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int
 template <int KIND, typename OutT>
 static cudaError_t launch_backward(const Launch& L, const BwdArgs<KIND>& args, int64_t max_tiles) {
   auto kern = ffn_backward_kernel<KIND, OutT>;
-  const cudaError_t e = allow_smem<ffn_backward_kernel<KIND, OutT>>(BwdLayout::SMEM);
+  const cudaError_t e = allow_smem<ffn_backward_kernel<KIND, OutT>>(BwdLayout<KIND>::SMEM);
   if (e != cudaSuccess) return e;
-  pdl_launch(kern, dim3(static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms))), dim3(kGemmThreads),
-             BwdLayout::SMEM, L.stream, args);
+  pdl_launch(kern, dim3(static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms))), dim3(kBwdThreads),
+             BwdLayout<KIND>::SMEM, L.stream, args);
   count_launch();
   return cudaGetLastError();
 }
@@ -153,8 +153,6 @@ static BwdArgs<KIND> backward_args(const Launch& L, int64_t R, int E, int k_dim,
   return a;
 }
 
-static int64_t column_blocks(int n) { return (n + bwd_tile_n(n) - 1) / bwd_tile_n(n); }
-
 static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
                                         const int32_t* off, const ExpertWeights& w, const Activation& act,
                                         const void* gu, const void* h, const void* dy, void* dgu, void* dx,
@@ -168,8 +166,9 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     if ((e = make_tmap(&j.b0, w.w_down, false, F, D, E, kBwdBK)) != cudaSuccess) return e;
     j.out = dgu;
     j.n = F;
+    j.nt = bwd_col_blocks(F, false);
     a.gu = static_cast<const __nv_bfloat16*>(gu);
-    if ((e = launch_backward<BWD_DH, __nv_bfloat16>(L, a, max_row_blocks(R, E) * column_blocks(F))) != cudaSuccess)
+    if ((e = launch_backward<BWD_DH, __nv_bfloat16>(L, a, max_row_blocks(R, E) * j.nt)) != cudaSuccess)
       return e;
   }
   if (dx != nullptr) {
@@ -180,7 +179,8 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     if ((e = make_tmap(&j.b1, w.w_up, false, D, F, E, kBwdBK)) != cudaSuccess) return e;
     j.out = dx;
     j.n = D;
-    if ((e = launch_backward<BWD_DX, __nv_bfloat16>(L, a, max_row_blocks(R, E) * column_blocks(D))) != cudaSuccess)
+    j.nt = bwd_col_blocks(D, false);
+    if ((e = launch_backward<BWD_DX, __nv_bfloat16>(L, a, max_row_blocks(R, E) * j.nt)) != cudaSuccess)
       return e;
   }
   BwdArgs<BWD_DW> a = backward_args<BWD_DW>(L, R, E, 0, off, act);
@@ -193,7 +193,8 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     j.bias_out = bias_out;
     j.m = m;
     j.n = n;
-    tiles += int64_t(E) * ((m + kBM - 1) / kBM) * column_blocks(n);
+    j.nt = bwd_col_blocks(n, bias_out != nullptr);
+    tiles += int64_t(E) * ((m + kBM - 1) / kBM) * j.nt;
     const cudaError_t r = make_tmap_rows(&j.a, pa, m, R, lda);
     return r != cudaSuccess ? r : make_tmap_rows(&j.b0, pb, n, R, n);
   };
