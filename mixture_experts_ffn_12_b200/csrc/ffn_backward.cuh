@@ -10,30 +10,40 @@
 //       none), and the bias gradients, the column sums of dy, dg, du over the same rows.
 //
 // Operand orders: the weights are stored [N, K] for the forward pass, so here the reduction
-// runs along their slow dimension: B is "MN-major" (N contiguous), which the tensor core
-// reads directly (instruction descriptor transpose bits, 128-byte swizzle: 64 N-elements x
-// 8 K-rows per 1024-byte atom).  DW has both operands MN-major, its K running over rows.
-// TMA brings [64 K-rows x 64 elements] boxes; no operand is transposed in memory.
-//
+// runs along their slow dimension: "MN-major" operands (output index contiguous), which the
+// tensor core reads directly (instruction descriptor transpose bits, 128-byte swizzle: 64
+// elements x 8 K-rows per 1024-byte atom) at the rate of K-major ones.  DW has both operands
+// MN-major, its K running over rows.  TMA brings [64 K-rows x 64 elements] boxes; nothing is
+// transposed in memory.  DH and DX put the weights in M (their output transposed, 256 output
+// columns a tile) and the expert's rows in N, split evenly into tiles of at most 256 in steps
+// of 16: a ragged expert wastes at most 15 rows of MMA work a tile, where rows in M would
+// round every expert up to 128 or 256.
+
 // DW's K range is an expert's row range, of any length.  Its last block may reach into
 // rows of the next expert: whole 16-row MMA steps past the end are not issued, and the
 // rows past the end of the last step are overwritten with zeros in shared memory, in both
 // operands, before the MMA reads them (zeroing one would let an infinity or a NaN of a
 // neighbouring expert through as 0 * inf).
 //
-// Bias gradients: for the tiles of the first column block, which DW keeps at most 192
-// columns wide, the issuer adds one N = 16 MMA a step whose B operand is a tile of ones, into
-// TMEM columns that the tile leaves free: the sums cost no further pass over dy and dgu.
+// Bias gradients: for the tiles of the first column block, which DW keeps 128 columns wide,
+// the issuer adds one N = 16 MMA a step whose B operand is a tile of ones, into TMEM columns
+// that the tile leaves free: the sums cost no further pass over dy and dgu.
 //
 // dg and du are rounded to bf16 between DH and the two products that read them (they are
 // tensor-core operands); all sums are fp32.
 //
-// Tile 128 x (64 to 256 columns): the columns are split into blocks of 1 to 4 boxes of 64,
-// as even as that allows (2880 = 3 x 192 + 9 x 256), so that every box row is one 128-byte
-// line of L2 -- evener blocks of 240 columns start between lines, and each box row then
-// takes two L2 requests.  Four 64-deep stages, two accumulator buffers; roles as in
-// grouped_gemm.cuh.  DH and DX walk (expert, row block, column block) tiles of the ragged
-// rows, DW walks (matrix, expert, 128-row block, column block) tiles of the gradients.
+// CTA pairs (cta_group::2): a tile of M = 256 x N <= 256 a pair, every CTA staging its own 128
+// rows of A and half of B, 32 KB a 64-deep stage where a CTA alone takes 48 KB for the same
+// MMA time.  DW's columns are split into blocks of 256 and 128 (narrow ones first), so that
+// every box row is one 128-byte line.
+//
+// Roles (384 threads a CTA): warp 0 TMA producer; warp 1 TMEM and, in the leader, the MMA
+// issuer; warps 2..9 epilogue of the CTA's own 128 accumulator rows; warp 10 the tile scheduler, which
+// decodes tiles ahead of everyone into a ring (decoding costs some 500 cycles of division,
+// a DW tile of a few hundred rows only some thousands); warp 11 blanks tails (DW) or
+// prefetches g and u (DH).  Waits
+// bounded as in grouped_gemm.cuh, two accumulator buffers, and the closing cluster barrier of
+// grouped_gemm_pair.cuh.
 #pragma once
 
 #include "grouped_gemm_mx4.cuh"
@@ -42,11 +52,11 @@ namespace moe {
 
 enum BwdKind : int { BWD_DH = 0, BWD_DX = 1, BWD_DW = 2 };
 
+constexpr int kBwdBM = 256;          // M of a pair's tile, and the most rows in its N (DH, DX)
 constexpr int kBwdBK = 64;           // K per stage
-constexpr int kBwdStages = 4;
+constexpr int kBwdStages = 6;
 constexpr int kBwdBox = 64 * 128;    // bytes of a [64 K-rows x 64 elements] box
-constexpr int kBwdOnesCol = 192;     // TMEM column of the bias sums inside an accumulator buffer
-
+constexpr int kBwdOnesCol = 128;     // TMEM column of the bias sums inside an accumulator buffer
 constexpr int kBwdThreads = 384;
 constexpr int kBwdEpiWarps = 8;
 constexpr int kBwdSched = 4;         // tiles the scheduler is ahead
@@ -54,39 +64,50 @@ constexpr int kBwdSched = 4;         // tiles the scheduler is ahead
 template <int KIND>
 struct BwdLayout {
   static constexpr int A_BYTES = 2 * kBwdBox;
-  static constexpr int B_BYTES = 4 * kBwdBox;
+  static constexpr int B_BYTES = 2 * kBwdBox;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int ONES = KIND == BWD_DW ? 2048 : 0;                     // 16 rows x 128 B of bf16 ones
-  // epilogue staging of a warp: 32 rows of 64 B + 16 B;  DH: of g and u, 32 B + 16 B each
-  static constexpr int STAGING_WARP = KIND == BWD_DH ? 2 * 32 * 48 : 32 * 80;
+  static constexpr int ONES = KIND == BWD_DW ? 1024 : 0;   // 8 rows x 128 B of bf16 ones: half of N = 16
+  static constexpr int STAGING_WARP = KIND == BWD_DW ? 32 * 80 : 0;   // epilogue: 32 rows of 64 B + 16 B
   static constexpr int STAGING = kBwdEpiWarps * STAGING_WARP;
   static constexpr int EXTRA = 1024 + 3072;
   static constexpr int SMEM = kBwdStages * STAGE_BYTES + ONES + STAGING + EXTRA;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-// Column blocks of N columns: 1 to 4 boxes of 64 each (3 at most for the first one if
-// `spare`), differing by at most one box, the narrower ones first.
+// Column blocks of N columns: 1 or 2 units of 128 each (1 for the first one if `spare`), the
+// narrower ones first.
 __host__ __device__ constexpr int bwd_col_blocks(int N, bool spare) {
-  return ((N + 63) / 64 + (spare ? 1 : 0) + 3) / 4;
+  return ((N + 127) / 128 + (spare ? 1 : 0) + 1) / 2;
 }
 struct BwdCols {
-  int first, boxes;   // first column, number of 64-column boxes
+  int first, units;   // first column, number of 128-column units
 };
 __host__ __device__ inline BwdCols bwd_cols(int N, int blocks, int j) {
-  const int n64 = (N + 63) / 64;
-  const int q = n64 / blocks, narrow = blocks - n64 % blocks;
-  return BwdCols{64 * (j * q + (j > narrow ? j - narrow : 0)), q + (j >= narrow ? 1 : 0)};
+  const int n = (N + 127) / 128;
+  const int q = n / blocks, narrow = blocks - n % blocks;
+  return BwdCols{128 * (j * q + (j > narrow ? j - narrow : 0)), q + (j >= narrow ? 1 : 0)};
 }
 
-// One product of a launch.  DH: A = dy, B0 = Wd.  DX: A = dgu (halves), B0 = Wg, B1 = Wu.
-// DW: A, B0 = the two row-major operands whose rows are summed over.
+// One product of a launch.  DW: a, b[0] = the two row-major operands whose rows are summed
+// over.  DH: a = Wd, b = dy.  DX: a, a2 = Wg, Wu, b = dgu; b[q] has boxes of 64 K elements x
+// 32 (q + 1) rows.
+// Two boxes of a K-rows x elements operand come in one copy: the matrix seen as {64 columns,
+// K rows, N / 64} (and groups), a box of 64 x 64 x 2 landing as consecutive [64 x 64] boxes.
+// Where the partial box of an N that is no multiple of 64 is met, and for one box alone, the
+// copies are single boxes.  (One TMA instruction costs the producer thread some 100 cycles.)
+struct BwdMaps {
+  CUtensorMap two, single;
+};
 struct BwdJob {
-  CUtensorMap a, b0, b1;
+  BwdMaps a, a2;
+  union {
+    BwdMaps bw;         // DW
+    CUtensorMap b[4];   // DH, DX
+  };
   void* out;
   void* bias_out;   // DW: [G, m] column sums of A, or null
-  int m, n;         // DW: rows and columns of the gradient;  DH, DX: n = columns of the output
-  int nt;           // column blocks
+  int m, n;         // DW: rows and columns of the gradient;  DH, DX: m = columns of the output
+  int nt;           // DW: column blocks
 };
 
 template <int KIND>
@@ -101,6 +122,22 @@ struct BwdArgs {
   float limit, alpha, gate_lo;
   unsigned long long wait_limit_ns;
 };
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const void* tmap, uint32_t bar_cluster, int c0, int c1,
+                                                 int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 
 // K-rows x elements operand ("MN-major"), 128-byte swizzle: 64-element blocks kBwdBox bytes
 // apart (leading offset), 8-row groups 1024 bytes apart (stride offset).
@@ -126,45 +163,66 @@ __device__ __forceinline__ void act_grad(float dh, float g, float u, float limit
 
 struct BwdTile {
   int job, g;           // job -1: no more tiles
-  int m0, m_end;        // DW: rows of the gradient;  DH, DX: rows of A
-  int n0, boxes;        // first column, 64-column boxes
+  int m0;               // first row of the gradient (DW), first column of the output (DH, DX)
+  int n0, units;        // DW: first column, 128-column units
+  int n;                // MMA N
   int kb;               // 64-deep K blocks
-  int r0, rows;         // DW: the expert's rows
+  int r0, rows;         // DW: the expert's rows;  DH, DX: the tile's
+  int sums;             // DW: bias gradients wanted of this tile
 };
+
+// DW: the last K block of the tile ends inside a 16-row MMA step.
+__device__ __forceinline__ bool bwd_ragged(const BwdTile& t) { return (t.rows & 15) != 0; }
 
 template <int KIND>
 __device__ __forceinline__ BwdTile bwd_tile(int i, const int* tile_off, const int* goff, const BwdArgs<KIND>& a) {
-  BwdTile t;
-  t.job = 0;
-  int nb;
+  BwdTile t{};
   if constexpr (KIND == BWD_DW) {
-    int mt = 0;
+    int mt, nt;
     for (;; ++t.job) {
-      mt = (a.job[t.job].m + kBM - 1) / kBM;
-      const int n = a.num_groups * mt * a.job[t.job].nt;
+      nt = a.job[t.job].nt;
+      mt = (a.job[t.job].m + kBwdBM - 1) / kBwdBM;
+      const int n = a.num_groups * mt * nt;
       if (i < n || t.job + 1 == a.num_jobs) break;
       i -= n;
     }
-    const int nt = a.job[t.job].nt;
     t.g = i / (mt * nt);
     i -= t.g * mt * nt;
-    // bands of kGroupBand row blocks, the row block fastest: neighbours share operand rows in L2
-    const int band = i / (kGroupBand * nt);
-    const int rem = i - band * kGroupBand * nt;
-    const int rows = min(kGroupBand, mt - band * kGroupBand);
-    nb = rem / rows;
-    t.m0 = (band * kGroupBand + rem - nb * rows) * kBM;
-    t.m_end = a.job[t.job].m;
+    // bands of row blocks, the row block fastest: neighbours share operand rows in L2
+    constexpr int kBand = 8;
+    const int band = i / (kBand * nt);
+    const int rem = i - band * kBand * nt;
+    const int rows = min(kBand, mt - band * kBand);
+    const int nb = rem / rows;
+    t.m0 = (band * kBand + rem - nb * rows) * kBwdBM;
+    const BwdCols c = bwd_cols(a.job[t.job].n, nt, nb);
+    t.n0 = c.first;
+    t.units = c.units;
+    t.n = 128 * c.units;
+    t.r0 = goff[t.g];
+    t.rows = max(0, goff[t.g + 1] - t.r0);
+    t.kb = (t.rows + kBwdBK - 1) / kBwdBK;
+    t.sums = t.n0 == 0 && a.job[t.job].bias_out != nullptr ? 1 : 0;
   } else {
-    const TileInfo ti = decode_tile(i, tile_off, goff, a.num_groups, a.job[0].nt, 1);
-    t.g = ti.g;
-    t.m0 = ti.m0;
-    t.m_end = ti.m_end;
-    nb = ti.n0;
+    // tiles of an expert: its row tiles fastest (they share the weight columns)
+    const int mt = (a.job[0].m + kBwdBM - 1) / kBwdBM;
+    int lo = 0, hi = a.num_groups;            // tile_off[lo] * mt <= i < tile_off[hi] * mt
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile_off[mid] * mt <= i) lo = mid; else hi = mid;
+    }
+    t.g = lo;
+    const int rt = tile_off[lo + 1] - tile_off[lo], rows = goff[lo + 1] - goff[lo];
+    i -= tile_off[lo] * mt;
+    const int mb = i / rt, r = i - mb * rt;
+    const int per = ((rows + rt - 1) / rt + 15) / 16 * 16;
+    t.m0 = mb * kBwdBM;
+    t.r0 = goff[lo] + r * per;
+    t.rows = min(per, rows - r * per);
+    t.n = (t.rows + 15) / 16 * 16;
+    const int kb = (a.k_dim + kBwdBK - 1) / kBwdBK;
+    t.kb = KIND == BWD_DX ? 2 * kb : kb;
   }
-  const BwdCols c = bwd_cols(a.job[t.job].n, a.job[t.job].nt, nb);
-  t.n0 = c.first;
-  t.boxes = c.boxes;
   return t;
 }
 
@@ -199,18 +257,19 @@ __device__ __forceinline__ void store_rows64(uint8_t* stage, T* out, size_t ldo,
 }
 
 template <int KIND, typename OutT>
-__global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __grid_constant__ BwdArgs<KIND> args) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
+    ffn_backward_kernel(const __grid_constant__ BwdArgs<KIND> args) {
   pdl_enter();
   using LY = BwdLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ones = smem + kBwdStages * LY::STAGE_BYTES;
   uint8_t* staging = ones + LY::ONES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + LY::STAGING);
-  uint64_t* ready = full + kBwdStages;          // DW: the blanker has seen the stage
-  uint64_t* empty = ready + kBwdStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + LY::STAGING);   // leader's: both CTAs' stage is in place
+  uint64_t* landed = full + kBwdStages;         // DW: a ragged tail's loads have landed in this CTA
+  uint64_t* empty = landed + kBwdStages;
   uint64_t* tfull = empty + kBwdStages;
-  uint64_t* tempty = tfull + 2;
+  uint64_t* tempty = tfull + 2;                 // leader's
   uint64_t* sfull = tempty + 2;                 // scheduler ring
   uint64_t* sempty = sfull + kBwdSched;
   uint64_t* drain = sempty + kBwdSched;
@@ -223,23 +282,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());   // 0 = leader (issues the MMAs)
   const int G = args.num_groups;
   const uint64_t lim = args.wait_limit_ns;
-  constexpr int kConsumers = 2 + kBwdEpiWarps + (KIND == BWD_DW ? 1 : 0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kBwdStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&ready[s], 1);
+      mbar_init(&full[s], 2);      // one arrival a CTA: its producer's, or its blanker's
+      mbar_init(&landed[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 32 * kBwdEpiWarps);
+      mbar_init(&tempty[b], 2 * kBwdEpiWarps);
     }
     for (int q = 0; q < kBwdSched; ++q) {
       mbar_init(&sfull[q], 1);
-      mbar_init(&sempty[q], kConsumers);
+      mbar_init(&sempty[q], 1 + (rank == 0 ? 1 : 0) + kBwdEpiWarps + (KIND == BWD_DX ? 0 : 1));   // who reads a tile
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -248,24 +307,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    mx4_group_table(args.group_off, G, args.m_total, goff, tile_off);
+    mx4_group_table<kBwdBM>(args.group_off, G, args.m_total, goff, tile_off);
     if (lane < args.num_jobs) {
-      tma_prefetch_desc(&args.job[lane].a);
-      tma_prefetch_desc(&args.job[lane].b0);
-      if (KIND == BWD_DX) tma_prefetch_desc(&args.job[lane].b1);
+      tma_prefetch_desc(&args.job[lane].a.single);
+      tma_prefetch_desc(KIND == BWD_DW ? &args.job[lane].bw.single : &args.job[lane].b[3]);
     }
   } else if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
   } else if (KIND == BWD_DW && warp < 6) {
     for (int i = threadIdx.x - 64; i < LY::ONES / 4; i += 128) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int KB1 = (args.k_dim + kBwdBK - 1) / kBwdBK;   // DH, DX: K blocks (of one half)
+  const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+  const int KB1 = (args.k_dim + kBwdBK - 1) / kBwdBK;   // DX: K blocks of one half
 
   // The next tile from the scheduler's ring; false when a wait gave up.  One thread, or a
   // whole warp (which then agrees on the answer).
@@ -286,20 +346,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
     if (lane == 0) {
       int total = 0;
       if constexpr (KIND == BWD_DW) {
-        for (int j = 0; j < args.num_jobs; ++j) total += G * ((args.job[j].m + kBM - 1) / kBM) * args.job[j].nt;
+        for (int j = 0; j < args.num_jobs; ++j) total += G * ((args.job[j].m + kBwdBM - 1) / kBwdBM) * args.job[j].nt;
       } else {
-        total = tile_off[G] * args.job[0].nt;
+        total = tile_off[G] * ((args.job[0].m + kBwdBM - 1) / kBwdBM);
       }
       int n = 0;
-      for (int i = blockIdx.x;; i += gridDim.x, ++n) {
+      for (int i = blockIdx.x >> 1;; i += gridDim.x >> 1, ++n) {
         BwdTile t;
         t.job = -1;
-        if (i < total) {
-          t = bwd_tile<KIND>(i, tile_off, goff, args);
-          t.r0 = goff[t.g];
-          t.rows = max(0, goff[t.g + 1] - t.r0);
-          t.kb = KIND == BWD_DW ? (t.rows + kBwdBK - 1) / kBwdBK : KIND == BWD_DX ? 2 * KB1 : KB1;
-        }
+        if (i < total) t = bwd_tile<KIND>(i, tile_off, goff, args);
         const int q = n % kBwdSched;
         if (!mbar_wait(&sempty[q], ((n / kBwdSched) & 1) ^ 1, abort_flag, lim)) { ok = false; break; }
         ring[q] = t;
@@ -313,34 +368,65 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
     }
     __syncwarp();
   } else if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
       int s = 0;
-      uint32_t ph = 0, issued = 0, issued_par = 0;
+      uint32_t ph = 0, issued = 0, issued_par = 0;         // stages counted on the leader's full
+      uint32_t tails = 0, tail_par = 0, tail_uses = 0;     // stages counted on this CTA's landed
       BwdTile ti;
       for (int n = 0;; ++n) {
         if (!next_tile(n, ti, false)) { ok = false; break; }
         if (ti.job < 0) break;
         const BwdJob& jb = args.job[ti.job];
+        const int a_row = ti.m0 + rank * 128;
+        const bool a_two = a_row + 128 <= (jb.m & ~63) || (jb.m & 63) == 0;
+        const int b_col = ti.n0 + rank * 64 * ti.units;                       // DW
+        const bool b_two = ti.units == 2 && b_col + 128 <= (jb.n & ~63);
+        const int b_row = ti.r0 + rank * (ti.n / 2), q32 = (ti.n + 63) / 64;   // DH, DX: boxes of 32 rows
+        const uint32_t tx = LY::A_BYTES + (KIND == BWD_DW ? ti.units * kBwdBox : q32 * (kBwdBox / 2));
         for (int kb = 0; kb < ti.kb; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[s], LY::A_BYTES + ti.boxes * kBwdBox);
           uint8_t* sa = smem + s * LY::STAGE_BYTES;
           uint8_t* sb = sa + LY::A_BYTES;
-          if constexpr (KIND == BWD_DW) {
+          const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
+          if (KIND == BWD_DW && kb == ti.kb - 1 && bwd_ragged(ti)) {
+            // the blanker is told here, and passes the stage on to the leader
             const int r = ti.r0 + kb * kBwdBK;
-            for (int q = 0; q < ti.boxes; ++q) tma_load_2d(sb + q * kBwdBox, &jb.b0, &full[s], ti.n0 + 64 * q, r);
-            for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kBwdBox, &jb.a, &full[s], ti.m0 + 64 * q, r);
+            mbar_arrive_expect_tx(&landed[s], tx);
+            if (b_two) tma_load_3d(sb, &jb.bw.two, &landed[s], 0, r, b_col / 64);
+            else
+              for (int q = 0; q < ti.units; ++q) tma_load_2d(sb + q * kBwdBox, &jb.bw.single, &landed[s], b_col + 64 * q, r);
+            if (a_two) tma_load_3d(sa, &jb.a.two, &landed[s], 0, r, a_row / 64);
+            else
+              for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kBwdBox, &jb.a.single, &landed[s], a_row + 64 * q, r);
+            issued &= ~(1u << s);   // its earlier loads have landed, or the slot were not free
+            tails |= 1u << s;
+            tail_par = (tail_par & ~(1u << s)) | (tail_uses & (1u << s));
+            tail_uses ^= 1u << s;
           } else {
-            const int half = (KIND == BWD_DX && kb >= KB1) ? 1 : 0;
-            const int k0 = (kb - half * KB1) * kBwdBK;
-            const CUtensorMap* tb = half ? &jb.b1 : &jb.b0;
-            for (int q = 0; q < ti.boxes; ++q) tma_load_3d(sb + q * kBwdBox, tb, &full[s], ti.n0 + 64 * q, k0, ti.g);
-            if (KIND == BWD_DX) tma_load_3d(sa, &jb.a, &full[s], k0, half, ti.m0);
-            else tma_load_2d(sa, &jb.a, &full[s], k0, ti.m0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * tx);
+            else mbar_arrive_cluster(fb);
+            if constexpr (KIND == BWD_DW) {
+              const int r = ti.r0 + kb * kBwdBK;
+              if (b_two) tma_load_3d_pair(sb, &jb.bw.two, fb, 0, r, b_col / 64);
+              else
+                for (int q = 0; q < ti.units; ++q) tma_load_2d_pair(sb + q * kBwdBox, &jb.bw.single, fb, b_col + 64 * q, r);
+              if (a_two) tma_load_3d_pair(sa, &jb.a.two, fb, 0, r, a_row / 64);
+              else
+                for (int q = 0; q < 2; ++q) tma_load_2d_pair(sa + q * kBwdBox, &jb.a.single, fb, a_row + 64 * q, r);
+            } else {
+              const int half = (KIND == BWD_DX && kb >= KB1) ? 1 : 0;
+              const int k0 = (kb - half * KB1) * kBwdBK;
+              const BwdMaps& ma = half ? jb.a2 : jb.a;
+              if (a_two) tma_load_4d_pair(sa, &ma.two, fb, 0, k0, a_row / 64, ti.g);
+              else
+                for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * kBwdBox, &ma.single, fb, a_row + 64 * q, k0, ti.g);
+              if (KIND == BWD_DX) tma_load_3d_pair(sb, &jb.b[q32 - 1], fb, k0, half, b_row);
+              else tma_load_2d_pair(sb, &jb.b[q32 - 1], fb, k0, b_row);
+            }
+            issued |= 1u << s;
+            issued_par = (issued_par & ~(1u << s)) | (ph << s);
           }
-          issued |= 1u << s;
-          issued_par = (issued_par & ~(1u << s)) | (ph << s);
           if (++s == kBwdStages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
@@ -348,38 +434,43 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
+        // the peer's barrier cannot be polled from here: give loads in flight time to land
+        for (int q = 0; q < 2000; ++q) __nanosleep(1000);
       }
-      for (int q = 0; q < kBwdStages; ++q)
-        if ((issued >> q) & 1u)
+      for (int q = 0; q < kBwdStages; ++q) {
+        if (rank == 0 && ((issued >> q) & 1u))
           if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+        if ((tails >> q) & 1u)
+          if (!mbar_wait(&landed[q], (tail_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer (leader only)
     // One thread issues every MMA (128 cycles each at 256 columns): descriptors are made
     // once and stepped by additions (built per MMA they took 264 cycles an MMA).
-    if (lane == 0) {
+    if (rank == 0 && lane == 0) {
       const uint32_t s_addr = smem_u32(smem);
-      const uint64_t a_desc = KIND == BWD_DW ? sw128_mnmajor_desc(s_addr) : sw128_kmajor_desc(s_addr);
-      const uint64_t b_desc = sw128_mnmajor_desc(s_addr + LY::A_BYTES);
+      const uint64_t a_desc = sw128_mnmajor_desc(s_addr);
+      const uint64_t b_desc = KIND == BWD_DW ? sw128_mnmajor_desc(s_addr + LY::A_BYTES) : sw128_kmajor_desc(s_addr + LY::A_BYTES);
       const uint64_t ones_desc = sw128_kmajor_desc(smem_u32(ones));
-      constexpr int kAStep = KIND == BWD_DW ? 2048 / 16 : 32 / 16;   // of 16 K elements
-      const uint32_t idesc_ones = make_idesc(kBM, 16, 1u) | (1u << 15);
-      uint64_t* loaded = KIND == BWD_DW ? ready : full;
+      constexpr int kAStep = 2048 / 16, kBStep = KIND == BWD_DW ? 2048 / 16 : 32 / 16;   // of 16 K elements
+      const uint32_t idesc_ones = make_idesc(kBwdBM, 16, 1u) | (1u << 15);
       int s = 0;
       uint32_t ph = 0;
+      bool issued_any = false;
       BwdTile ti;
       for (int n = 0;; ++n) {
         if (!next_tile(n, ti, false)) { ok = false; break; }
         if (ti.job < 0) break;
-        const uint32_t idesc = make_idesc(kBM, 64 * ti.boxes, 1u) | (1u << 16) | (KIND == BWD_DW ? 1u << 15 : 0u);
-        const bool sums = KIND == BWD_DW && ti.n0 == 0 && args.job[ti.job].bias_out != nullptr;
+        const uint32_t idesc = make_idesc(kBwdBM, ti.n, 1u) | (1u << 15) | (KIND == BWD_DW ? 1u << 16 : 0u);
+        const bool sums = KIND == BWD_DW && ti.sums != 0;
         const int acc = n & 1;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
-        if (!mbar_wait(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        if (!mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
         tc_fence_after();
         for (int kb = 0; kb < ti.kb; ++kb) {
-          if (!mbar_wait(&loaded[s], ph, abort_flag, lim)) { ok = false; break; }
+          if (!mbar_wait(&full[s], ph, abort_flag, lim)) { ok = false; break; }
           tc_fence_after();
           const uint64_t so = static_cast<uint64_t>(s * (LY::STAGE_BYTES >> 4));
           const uint64_t ad = a_desc + so, bd = b_desc + so;
@@ -387,113 +478,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
           if (steps == kBwdBK / 16 && !sums) {
 #pragma unroll
             for (int kk = 0; kk < kBwdBK / 16; ++kk)
-              tc_mma<false>(d_tmem, ad + kk * kAStep, bd + kk * 128, idesc, (kb | kk) != 0 ? 1u : 0u);
+              tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
           } else {
             for (int kk = 0; kk < steps; ++kk) {
               const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
-              tc_mma<false>(d_tmem, ad + kk * kAStep, bd + kk * 128, idesc, accumulate);
-              if (sums) tc_mma<false>(d_tmem + kBwdOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
+              tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate);
+              if (sums) tc_mma_pair(d_tmem + kBwdOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
             }
           }
-          tc_commit(&empty[s]);
+          issued_any = true;
+          tc_commit_pair_mc(&empty[s], 0x3);
           if (++s == kBwdStages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        tc_commit(&tfull[acc]);
+        tc_commit_pair_mc(&tfull[acc], 0x3);
       }
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
       }
-      tc_commit(drain);
-      if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+      if (issued_any) {
+        tc_commit_pair(drain);
+        if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+      }
     }
     __syncwarp();
   } else if (warp < 2 + kBwdEpiWarps) {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     // Two warps share a TMEM lane quarter and take its column chunks in turn.
+    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stage = staging + (warp - 2) * LY::STAGING_WARP;
     BwdTile ti;
     for (int n = 0;; ++n) {
       if (!next_tile(n, ti, true)) { ok = false; break; }
       if (ti.job < 0) break;
       const BwdJob& jb = args.job[ti.job];
       const int acc = n & 1;
-      const int row0 = ti.m0 + quarter * 32;
-      const int rows = ti.m_end - row0;
-      const int width = min(64 * ti.boxes, jb.n - ti.n0);
+      const int row0 = ti.m0 + rank * 128 + quarter * 32;   // of the warp's accumulator rows
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kAccStride);
-      if constexpr (KIND == BWD_DH) {
-        // 16 columns at a time: g and u come in 32-byte runs of rows (the next chunk's while
-        // this one is computed, the first before the accumulator is complete), turn into row
-        // order through the staging area, and dg and du leave the same way
-        const int F = jb.n;
-        const int r2 = lane >> 1, piece = lane & 1;
-        const __nv_bfloat16* gu = args.gu + static_cast<size_t>(row0) * 2 * F + ti.n0 + piece * 8;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + static_cast<size_t>(row0) * 2 * F + ti.n0 + piece * 8;
-        uint8_t* su = stage + 32 * 48;         // u's half of the warp's staging
-        uint4 pre[4];
-        auto fetch = [&](int c) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int r = p * 16 + r2;
-            pre[p] = pre[2 + p] = make_uint4(0, 0, 0, 0);
-            if (c < width && r < rows) {
-              pre[p] = *reinterpret_cast<const uint4*>(gu + static_cast<size_t>(r) * 2 * F + c);
-              pre[2 + p] = *reinterpret_cast<const uint4*>(gu + static_cast<size_t>(r) * 2 * F + F + c);
-            }
-          }
-        };
-        fetch(16 * half);
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 16 * half; c < width; c += 32) {
-          __syncwarp();
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            *reinterpret_cast<uint4*>(stage + (p * 16 + r2) * 48 + piece * 16) = pre[p];
-            *reinterpret_cast<uint4*>(su + (p * 16 + r2) * 48 + piece * 16) = pre[2 + p];
-          }
-          __syncwarp();
-          fetch(c + 32);
-          float v[16];
-          tmem_ld8(tbase + c, *reinterpret_cast<float(*)[8]>(v));
-          tmem_ld8(tbase + c + 8, *reinterpret_cast<float(*)[8]>(v + 8));
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            float gv[8], uv[8], dg[8], du[8];
-            __nv_bfloat16* pg = reinterpret_cast<__nv_bfloat16*>(stage + lane * 48 + j * 2);
-            __nv_bfloat16* pu = reinterpret_cast<__nv_bfloat16*>(su + lane * 48 + j * 2);
-            load8<__nv_bfloat16>(pg, gv);
-            load8<__nv_bfloat16>(pu, uv);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              act_grad(v[j + q], gv[q], uv[q], args.limit, args.alpha, args.gate_lo, dg[q], du[q]);
-            store8<__nv_bfloat16>(pg, dg);
-            store8<__nv_bfloat16>(pu, du);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int r = p * 16 + r2;
-            if (r < rows) {
-              *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * 2 * F + c) =
-                  *reinterpret_cast<const uint4*>(stage + r * 48 + piece * 16);
-              *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * 2 * F + F + c) =
-                  *reinterpret_cast<const uint4*>(su + r * 48 + piece * 16);
-            }
-          }
-        }
-      } else {
+      if constexpr (KIND == BWD_DW) {
         constexpr int COLS = 64 / static_cast<int>(sizeof(OutT));
+        uint8_t* stage = staging + (warp - 2) * LY::STAGING_WARP;
+        const int rows = jb.m - row0, width = min(ti.n, jb.n - ti.n0);
         if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
         tc_fence_after();
-        const bool none = KIND == BWD_DW && ti.rows == 0;   // the gradient is zero
-        const size_t row_base = KIND == BWD_DW ? static_cast<size_t>(ti.g) * jb.m : 0;
+        const bool none = ti.rows == 0;   // the gradient is zero
+        const size_t row_base = static_cast<size_t>(ti.g) * jb.m;
         OutT* out = static_cast<OutT*>(jb.out) + (row_base + row0) * jb.n + ti.n0;
 #pragma unroll 1
         for (int c = COLS * half; c < width; c += 2 * COLS) {
@@ -507,7 +538,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
           }
           store_rows64<OutT>(stage, out + c, jb.n, rows, width - c, v);
         }
-        if (KIND == BWD_DW && half == 0 && ti.n0 == 0 && jb.bias_out != nullptr) {
+        if (half == 0 && ti.sums) {
           float b[8];
           tmem_ld8(tbase + kBwdOnesCol, b);
           tmem_ld_wait();
@@ -518,39 +549,114 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
             else *bo = sum;
           }
         }
+      } else {
+        // lane = output column, accumulator column = row: each access of the warp is a
+        // 64-byte run of one row.  16 rows at a time; DH's g and u of the next 16 are on
+        // their way while these are computed, the first before the accumulator is complete.
+        const int col = row0 + lane, M = jb.m;
+        const bool cvalid = col < M;
+        constexpr int kRowElems = KIND == BWD_DH ? 2 : 1;   // DH: [R, 2, F]
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + static_cast<size_t>(ti.r0) * kRowElems * M + col;
+        const __nv_bfloat16* gu = args.gu + static_cast<size_t>(ti.r0) * kRowElems * M + col;
+        const size_t ld = static_cast<size_t>(kRowElems) * M;
+        const int rows = cvalid ? ti.rows : 0;
+        __nv_bfloat16 pg[16], pu[16];
+        auto fetch = [&](int c) {
+          if constexpr (KIND == BWD_DH) {
+            const __nv_bfloat16* p = gu + c * ld;
+#pragma unroll
+            for (int j = 0; j < 16; ++j, p += ld)
+              if (c + j < rows) {
+                pg[j] = p[0];
+                pu[j] = p[M];
+              }
+          }
+        };
+        fetch(16 * half);
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 16 * half; c < ti.rows; c += 32) {
+          float v[16];
+          tmem_ld8(tbase + c, *reinterpret_cast<float(*)[8]>(v));
+          tmem_ld8(tbase + c + 8, *reinterpret_cast<float(*)[8]>(v + 8));
+          tmem_ld_wait();
+          __nv_bfloat16* o = out + c * ld;
+          if constexpr (KIND == BWD_DH) {
+            uint32_t d[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float dg, du;
+              act_grad(v[j], __bfloat162float(pg[j]), __bfloat162float(pu[j]), args.limit, args.alpha, args.gate_lo,
+                       dg, du);
+              const __nv_bfloat162 both = __floats2bfloat162_rn(dg, du);
+              d[j] = *reinterpret_cast<const uint32_t*>(&both);
+            }
+            fetch(c + 32);
+#pragma unroll
+            for (int j = 0; j < 16; ++j, o += ld)
+              if (c + j < rows) {
+                o[0] = __ushort_as_bfloat16(static_cast<uint16_t>(d[j]));
+                o[M] = __ushort_as_bfloat16(static_cast<uint16_t>(d[j] >> 16));
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, o += ld)
+              if (c + j < rows) o[0] = __float2bfloat16_rn(v[j]);
+          }
+        }
       }
       tc_fence_before();
-      mbar_arrive(&tempty[acc]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc) * 8u);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      flag_error(DEVERR_TIMEOUT);
+    }
+  } else if (KIND == BWD_DH) {
+    // ------------------------------------------------------------ prefetcher
+    // g and u of coming tiles into the L2: the epilogue's loads look only 16 rows ahead.
+    BwdTile ti;
+    for (int n = 0;; ++n) {
+      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (ti.job < 0) break;
+      const int F = args.job[0].m;
+      const int col = ti.m0 + rank * 128 + (lane & 1) * 64;
+      if (col < F)
+        for (int r = lane >> 1; r < 2 * ti.rows; r += 16)   // g and u of a row: two runs of F elements
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(args.gu + (static_cast<size_t>(ti.r0) * 2 + r) * F + col));
     }
     if (!ok) {
       *abort_flag = 1;
       flag_error(DEVERR_TIMEOUT);
     }
   } else if (KIND == BWD_DW) {
-    // ------------------------------------------------------------ blanker
-    // Passes every loaded stage on to the issuer, after blanking the rows between the end
-    // of the expert and the end of the last 16-row step.
+    // ------------------------------------------------------------ blanker (both CTAs)
+    // Blanks the rows between the end of an expert and the end of its last 16-row step in
+    // this CTA's operands, then makes the CTA's arrival on the leader's full barrier (the
+    // proxy fence publishes the writes to the tensor core, as in grouped_gemm_pair_mx.cuh).
     int s = 0;
-    uint32_t ph = 0;
+    uint32_t uses = 0;
     BwdTile ti;
-    for (int n = 0; ok; ++n) {
+    for (int n = 0;; ++n) {
       if (!next_tile(n, ti, true)) { ok = false; break; }
       if (ti.job < 0) break;
-      for (int kb = 0; kb < ti.kb; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, lim))) { ok = false; break; }
-        const int valid = ti.rows - kb * kBwdBK;
-        if (valid < kBwdBK && (valid & 15) != 0) {
-          uint8_t* st = smem + s * LY::STAGE_BYTES + valid * 128;
-          const int pieces = (16 - (valid & 15)) * 8;
-          for (int box = 0; box < 2 + ti.boxes; ++box)
-            for (int q = lane; q < pieces; q += 32)
-              *reinterpret_cast<uint4*>(st + box * kBwdBox + q * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();   // read by the tensor core (async proxy)
-        }
+      if (ti.kb > 0 && bwd_ragged(ti)) {
+        const int q = (s + ti.kb - 1) % kBwdStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&landed[q], (uses >> q) & 1u, abort_flag, lim))) { ok = false; break; }
+        uses ^= 1u << q;
+        const int valid = ti.rows - (ti.kb - 1) * kBwdBK;
+        uint8_t* st = smem + q * LY::STAGE_BYTES + valid * 128;
+        const int pieces = (16 - (valid & 15)) * 8;
+        for (int box = 0; box < 2 + ti.units; ++box)
+          for (int p = lane; p < pieces; p += 32)
+            *reinterpret_cast<uint4*>(st + box * kBwdBox + p * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();   // read by the tensor core (async proxy)
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ready[s]);
-        if (++s == kBwdStages) { s = 0; ph ^= 1u; }
+        if (lane == 0) mbar_arrive_cluster(full_leader + static_cast<uint32_t>(q) * 8u);
       }
+      s = (s + ti.kb) % kBwdStages;
     }
     if (!ok) {
       *abort_flag = 1;
@@ -560,9 +666,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ffn_backward_kernel(const __gr
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();   // no CTA leaves while its peer may still signal it or read its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, kTmemCols);
   }
 }
 

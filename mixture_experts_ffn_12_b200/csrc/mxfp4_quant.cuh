@@ -98,8 +98,9 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const T* __restrict
   }
 }
 
-// Row-group table of a kernel: goff[g] (clamped into [0, rows]) and the prefix of 128-row
+// Row-group table of a kernel: goff[g] (clamped into [0, rows]) and the prefix of BM-row
 // blocks per group.  Called by one whole warp; G <= kMaxGroups.
+template <int BM = kBM>
 __device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int rows, int* goff, int* blk) {
   const int lane = threadIdx.x & 31;
   int bad = 0;
@@ -117,7 +118,7 @@ __device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int r
     if (g < G) {
       const int n = goff[g + 1] - goff[g];
       if (n < 0) bad = 1;
-      cnt = n > 0 ? (n + kBM - 1) / kBM : 0;
+      cnt = n > 0 ? (n + BM - 1) / BM : 0;
     }
     int incl = cnt;
 #pragma unroll

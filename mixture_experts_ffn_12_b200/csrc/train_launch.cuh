@@ -37,18 +37,25 @@ static cudaError_t make_tmap_bytes(CUtensorMap* m, const void* ptr, uint64_t row
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// bf16 rows [rows, cols] that lie ld elements apart; boxes of 64 elements x 64 rows.
-static cudaError_t make_tmap_rows(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld) {
+// bf16 rows [groups, rows, cols] that lie ld elements apart (groups 0: one matrix), as a
+// K-rows x elements operand (ffn_backward.cuh): boxes of 64 columns x 64 rows, alone and in
+// pairs (only where the matrix has a whole box: below 64 columns no copy takes pairs).
+static cudaError_t make_bwd_maps(BwdMaps* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld,
+                                 uint64_t groups) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, 64};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int two = 0; two <= (cols >= 64 ? 1 : 0); ++two) {
+    const cuuint64_t dims_p[4] = {64, rows, cols / 64, groups}, dims_s[3] = {cols, rows, groups};
+    const cuuint64_t strides_p[3] = {ld * 2, 128, rows * ld * 2}, strides_s[2] = {ld * 2, rows * ld * 2};
+    const cuuint32_t box_p[4] = {64, 64, 2, 1}, box_s[3] = {64, 64, 1};
+    const CUresult r = fn(two ? &m->two : &m->single, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (groups ? 3 : 2) + two,
+                          const_cast<void*>(ptr), two ? dims_p : dims_s, two ? strides_p : strides_s,
+                          two ? box_p : box_s, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------
@@ -128,10 +135,10 @@ cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int
 
 template <int KIND, typename OutT>
 static cudaError_t launch_backward(const Launch& L, const BwdArgs<KIND>& args, int64_t max_tiles) {
-  auto kern = ffn_backward_kernel<KIND, OutT>;
+  auto kern = ffn_backward_kernel<KIND, OutT>;   // clusters of two CTAs
   const cudaError_t e = allow_smem<ffn_backward_kernel<KIND, OutT>>(BwdLayout<KIND>::SMEM);
   if (e != cudaSuccess) return e;
-  pdl_launch(kern, dim3(static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms))), dim3(kBwdThreads),
+  pdl_launch(kern, dim3(2 * static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms / 2))), dim3(kBwdThreads),
              BwdLayout<KIND>::SMEM, L.stream, args);
   count_launch();
   return cudaGetLastError();
@@ -153,6 +160,8 @@ static BwdArgs<KIND> backward_args(const Launch& L, int64_t R, int E, int k_dim,
   return a;
 }
 
+static int64_t bwd_row_tiles(int64_t R, int E) { return (R + kBwdBM - 1) / kBwdBM + E; }
+
 static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
                                         const int32_t* off, const ExpertWeights& w, const Activation& act,
                                         const void* gu, const void* h, const void* dy, void* dgu, void* dx,
@@ -162,25 +171,25 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   if (dx != nullptr || gr.w_gate != nullptr || gr.w_up != nullptr) {
     BwdArgs<BWD_DH> a = backward_args<BWD_DH>(L, R, E, D, off, act);
     BwdJob& j = a.job[0];
-    if ((e = make_tmap(&j.a, dy, false, D, R, 0, kBM)) != cudaSuccess) return e;
-    if ((e = make_tmap(&j.b0, w.w_down, false, F, D, E, kBwdBK)) != cudaSuccess) return e;
+    if ((e = make_bwd_maps(&j.a, w.w_down, F, D, F, E)) != cudaSuccess) return e;
+    for (int q = 0; q < 4; ++q)
+      if ((e = make_tmap(&j.b[q], dy, false, D, R, 0, 32 * (q + 1))) != cudaSuccess) return e;
     j.out = dgu;
-    j.n = F;
-    j.nt = bwd_col_blocks(F, false);
+    j.m = F;
     a.gu = static_cast<const __nv_bfloat16*>(gu);
-    if ((e = launch_backward<BWD_DH, __nv_bfloat16>(L, a, max_row_blocks(R, E) * j.nt)) != cudaSuccess)
+    if ((e = launch_backward<BWD_DH, __nv_bfloat16>(L, a, bwd_row_tiles(R, E) * ((F + kBwdBM - 1) / kBwdBM))) != cudaSuccess)
       return e;
   }
   if (dx != nullptr) {
     BwdArgs<BWD_DX> a = backward_args<BWD_DX>(L, R, E, F, off, act);
     BwdJob& j = a.job[0];
-    if ((e = make_tmap_halves(&j.a, dgu, F, R, kBM)) != cudaSuccess) return e;
-    if ((e = make_tmap(&j.b0, w.w_gate, false, D, F, E, kBwdBK)) != cudaSuccess) return e;
-    if ((e = make_tmap(&j.b1, w.w_up, false, D, F, E, kBwdBK)) != cudaSuccess) return e;
+    if ((e = make_bwd_maps(&j.a, w.w_gate, D, F, D, E)) != cudaSuccess) return e;
+    if ((e = make_bwd_maps(&j.a2, w.w_up, D, F, D, E)) != cudaSuccess) return e;
+    for (int q = 0; q < 4; ++q)
+      if ((e = make_tmap_halves(&j.b[q], dgu, F, R, 32 * (q + 1))) != cudaSuccess) return e;
     j.out = dx;
-    j.n = D;
-    j.nt = bwd_col_blocks(D, false);
-    if ((e = launch_backward<BWD_DX, __nv_bfloat16>(L, a, max_row_blocks(R, E) * j.nt)) != cudaSuccess)
+    j.m = D;
+    if ((e = launch_backward<BWD_DX, __nv_bfloat16>(L, a, bwd_row_tiles(R, E) * ((D + kBwdBM - 1) / kBwdBM))) != cudaSuccess)
       return e;
   }
   BwdArgs<BWD_DW> a = backward_args<BWD_DW>(L, R, E, 0, off, act);
@@ -194,9 +203,9 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     j.m = m;
     j.n = n;
     j.nt = bwd_col_blocks(n, bias_out != nullptr);
-    tiles += int64_t(E) * ((m + kBM - 1) / kBM) * j.nt;
-    const cudaError_t r = make_tmap_rows(&j.a, pa, m, R, lda);
-    return r != cudaSuccess ? r : make_tmap_rows(&j.b0, pb, n, R, n);
+    tiles += int64_t(E) * ((m + kBwdBM - 1) / kBwdBM) * j.nt;
+    const cudaError_t r = make_bwd_maps(&j.a, pa, m, R, lda, 0);
+    return r != cudaSuccess ? r : make_bwd_maps(&j.bw, pb, n, R, n, 0);
   };
   if ((e = add(gr.w_down, gr.b_down, dy, D, D, h, F)) != cudaSuccess) return e;
   if ((e = add(gr.w_gate, gr.b_gate, dg, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
