@@ -3,16 +3,23 @@
 // with both operands E2M1 with one E8M0 scale per 32 elements along K
 // (tcgen05.mma kind::mxf4, block scales applied by the tensor core, fp32 accumulators).
 //
-// Stage = 256 elements of K = one 128-byte swizzled row of packed codes: A 128 rows and B
-// 192 rows by TMA (plain byte boxes: the mxf4 MMA reads 4-bit operands packed), the scales
-// as ready-made 512-byte chunks (mxfp4_quant.cuh) by bulk copies, four MMAs of K = 64.
-// Why 192 columns: two accumulator buffers (so a tile's epilogue overlaps the next tile's
-// loads and MMAs) leave 128 of the 512 TMEM columns, and the scales of a stage take 24 of
-// them; 2 x 256 columns would leave none.  A tile starts at a multiple of 192, so every
-// second one starts in the middle of a 128-row scale chunk: its MMAs read the scales two
-// TMEM columns (64 rows) further on.
+// At four times the bf16 rate the tensor core outruns what the L2 delivers to an SM, and for
+// few rows the weights are a plain stream from HBM, so the tile is chosen for its bytes:
+// CTA pairs (cta_group::2) with the weights in M (256 output columns a pair, 128 a CTA) and
+// the group's rows in N, at most 192, half of them staged by each CTA: 31 KB a stage of 256 K
+// where a CTA alone would take 43 KB for the same MMA time, and a group's last tile only as
+// wide as its rows (a step of 16), so a decode batch pays for its weights only.  Why 192:
+// two accumulator buffers (a tile's epilogue overlaps the next tile's MMAs) leave 2 x 64 of
+// the 512 TMEM columns, and the scales of a stage take 24; 2 x 256 columns would leave none.
 //
-// Roles (one CTA per SM, 192 threads) and tile order as in grouped_gemm.cuh; waits bounded.
+// Stage = 256 elements of K = one 128-byte swizzled row of packed codes (plain byte boxes:
+// the mxf4 MMA reads 4-bit operands packed); the scales come as ready-made 512-byte chunks
+// (mxfp4_quant.cuh) by TMA, tcgen05.cp brings them to TMEM, four MMAs of K = 64.
+//
+// Roles (384 threads a CTA): warp 0 producer of the codes, warp 11 of the scales (a copy
+// instruction costs a thread some 100 cycles, a stage has four and 384 cycles of MMAs);
+// warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue; warp 10 the tile
+// scheduler.  Waits bounded and the closing cluster barrier as in grouped_gemm_pair.cuh.
 #pragma once
 
 #include "mxfp4_quant.cuh"
@@ -20,21 +27,23 @@
 namespace moe {
 
 constexpr int kMx4BK = 256;       // K elements per stage
-constexpr int kMx4TN = 192;       // output columns per tile
-constexpr int kMx4Stages = 4;
+constexpr int kMx4Stages = 7;
+constexpr int kMx4BM = 256;       // output columns of a pair's tile
+constexpr int kMx4Threads = 384;
+constexpr int kMx4EpiWarps = 8;
+constexpr int kMx4Sched = 4;      // tiles the scheduler is ahead
 
 struct Mx4Layout {
-  static constexpr int A_BYTES = kBM * 128;
-  static constexpr int B_BYTES = kMx4TN * 128;
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = kMx4Rows / 2 * 128;
   static constexpr int SFA_BYTES = 1024;          // 2 chunks of 128 K
-  static constexpr int SFB_BYTES = 2048;          // 2 row blocks x 2 chunks
+  static constexpr int SFB_BYTES = 2048;          // 2 chunks of 128 K x 2 of 128 rows
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int STAGING = 4 * 32 * 144;    // epilogue: 32 rows of 128 B (+ 16 B) a warp
-  static constexpr int EXTRA = 1024 + 4096;
-  static constexpr int SMEM = kMx4Stages * STAGE_BYTES + STAGING + EXTRA;
+  static constexpr int EXTRA = 1024 + 3072;
+  static constexpr int SMEM = kMx4Stages * STAGE_BYTES + EXTRA;
   // TMEM: accumulators at columns 0 and 256; scales of even / odd stages behind them:
-  // A 2 chunks x 4 columns, then B 2 chunks x 2 row blocks x 4 columns
-  static constexpr int SF_COL = kMx4TN;
+  // weights 2 chunks x 4 columns, then rows 2 chunks x 2 x 4 columns
+  static constexpr int SF_COL = kMx4Rows;
   static constexpr int SFB_COL = 8;
   static_assert(STAGE_BYTES % 1024 == 0, "stages keep the swizzle alignment");
   static_assert(SF_COL + 24 <= kAccStride, "scales fit behind an accumulator");
@@ -48,100 +57,83 @@ __host__ __device__ constexpr uint32_t make_idesc_mx4(int M, int N, uint32_t sf_
          ((static_cast<uint32_t>(M) >> 4) << 24) | (sf_id << 29);
 }
 
-__device__ __forceinline__ void tc_mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_mx4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
           d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
       : "memory");
 }
 
-// Contiguous bytes (a multiple of 16, both addresses 16-byte aligned) into shared memory.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// tc_cp_sf in both CTAs of the pair, each from its own shared memory to its own TMEM.
+__device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 struct Mx4Args {
+  CUtensorMap w;              // weight codes [G][n_out][K/2] bytes, boxes of 128 rows
+  CUtensorMap x[3];           // row codes [m_total][K/2] bytes, boxes of 32, 64, 96 rows
   const int32_t* group_off;   // [G+1]; null: one group of m_total rows
   int num_groups;
   int m_total;
   int n_out;
   int k_dim;
-  const uint8_t* tiles_a;     // scale tiles of A, row blocks counted group after group
-  int row_blocks;             // their number (clamp for offsets that are not ascending)
-  const uint8_t* tiles_w;     // scale tiles of W, [G][ceil(n_out / 128)] row blocks
+  CUtensorMap sw, sx;         // scale tiles of W, [G][ceil(n_out / 128)] row blocks, and of the row
+                              //   tiles: runs of 1024 and 2048 bytes, seen as rows of 256 B
+  int row_tiles;              // number of row tiles (clamp for offsets that are not ascending)
   const __nv_bfloat16* bias;  // [G, n_out] or null
   void* out;                  // [m_total, n_out]
   unsigned long long wait_limit_ns;
 };
 
-// Writes 32 rows x (8 * PIECES) columns that the warp's lanes hold (lane = row) through its
-// staging area, so that each store instruction covers whole 128-byte runs of rows.
-// T = bf16: 64 columns a call; float: 32.
-template <typename T>
-__device__ __forceinline__ void store_rows_staged(uint8_t* stage, T* out, size_t ldo, int rows, int cols,
-                                                  const float* v) {
-  constexpr int COLS = 128 / static_cast<int>(sizeof(T));
-  constexpr int PER = 16 / static_cast<int>(sizeof(T));   // columns per 16-byte piece
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    uint4 u;
-    if constexpr (sizeof(T) == 2) {
-      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[p * PER + 2 * j], v[p * PER + 2 * j + 1]);
-    } else {
-      u = make_uint4(__float_as_uint(v[p * PER]), __float_as_uint(v[p * PER + 1]), __float_as_uint(v[p * PER + 2]),
-                     __float_as_uint(v[p * PER + 3]));
-    }
-    *reinterpret_cast<uint4*>(stage + lane * 144 + p * 16) = u;
-  }
-  __syncwarp();
-  const int piece = lane & 7;
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int r = it * 4 + (lane >> 3);
-    if (r < rows && piece * PER < cols)
-      *reinterpret_cast<uint4*>(out + r * ldo + piece * PER) =
-          *reinterpret_cast<const uint4*>(stage + r * 144 + piece * 16);
-  }
-  (void)COLS;
-}
+struct Mx4Tile {
+  int g;                // -1: no more tiles
+  int m0;               // first output column
+  int r0, rows, n;      // first row, rows, MMA N
+  int xt;               // row tile (of the scales)
+};
 
 template <typename OutT>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-    grouped_gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                            const Mx4Args args) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
+    grouped_gemm_mx4_kernel(const __grid_constant__ Mx4Args args) {
   pdl_enter();
   using LY = Mx4Layout;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = smem + kMx4Stages * LY::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + LY::STAGING);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kMx4Stages * LY::STAGE_BYTES);   // leader's: both CTAs' stage
   uint64_t* empty = full + kMx4Stages;
   uint64_t* tfull = empty + kMx4Stages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* tempty = tfull + 2;                // leader's
+  uint64_t* rfull = tempty + 2;                // scheduler ring
+  uint64_t* rempty = rfull + kMx4Sched;
+  uint64_t* drain = rempty + kMx4Sched;
+  Mx4Tile* ring = reinterpret_cast<Mx4Tile*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kMx4Sched);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* never_flag = abort_flag + 1;
-  int* tile_off = never_flag + 2;              // [G+1]
-  int* goff = tile_off + (kMaxGroups + 2);     // [G+1]
+  int* tile_off = never_flag + 1;              // [G+1] row tiles before each group
+  int* goff = tile_off + (kMaxGroups + 1);     // [G+1]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());   // 0 = leader (issues the MMAs)
   const int G = args.group_off == nullptr ? 1 : args.num_groups;
-  const int NT = (args.n_out + kMx4TN - 1) / kMx4TN;
+  const int MT = (args.n_out + kMx4BM - 1) / kMx4BM;
   const int KB = (args.k_dim + kMx4BK - 1) / kMx4BK;
-  const int NBW = (args.n_out + kBM - 1) / kBM;      // row blocks of W's scale tiles
   const uint64_t lim = args.wait_limit_ns;
 
   if (threadIdx.x == 0) {
@@ -151,7 +143,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 128);
+      mbar_init(&tempty[b], 2 * kMx4EpiWarps);
+    }
+    for (int q = 0; q < kMx4Sched; ++q) {
+      mbar_init(&rfull[q], 1);
+      mbar_init(&rempty[q], 2 + (rank == 0 ? 1 : 0) + kMx4EpiWarps);   // who reads a tile
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -160,154 +156,252 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    mx4_group_table(args.group_off, G, args.m_total, goff, tile_off);
+    mx4_group_table<kMx4Rows>(args.group_off, G, args.m_total, goff, tile_off);
     if (lane == 0) {
-      tma_prefetch_desc(&tmA);
-      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&args.w);
+      tma_prefetch_desc(&args.x[0]);
+      tma_prefetch_desc(&args.x[2]);
+      tma_prefetch_desc(&args.sw);
+      tma_prefetch_desc(&args.sx);
     }
   } else if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = tile_off[G] * NT;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  // The next tile from the scheduler's ring; false when a wait gave up.  One thread, or a
+  // whole warp (which then agrees on the answer).
+  auto next_tile = [&](int n, Mx4Tile& t, bool whole_warp) {
+    const int q = n % kMx4Sched;
+    bool got = mbar_wait(&rfull[q], (n / kMx4Sched) & 1, abort_flag, lim);
+    if (whole_warp) got = __all_sync(0xffffffffu, got);
+    if (!got) return false;
+    t = ring[q];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(&rempty[q]);
+    return true;
+  };
+  bool ok = true;
+
+  if (warp == 10) {
+    // ------------------------------------------------------------ scheduler
     if (lane == 0) {
-      const size_t row_block = static_cast<size_t>(KB) * 1024;   // bytes of one row block of scale tiles
+      const int total = tile_off[G] * MT;
+      int n = 0;
+      for (int i = blockIdx.x >> 1;; i += gridDim.x >> 1, ++n) {
+        Mx4Tile t{};
+        t.g = -1;
+        if (i < total) {
+          int lo = 0, hi = G;                  // tile_off[lo] * MT <= i < tile_off[hi] * MT
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tile_off[mid] * MT <= i) lo = mid; else hi = mid;
+          }
+          // a group's row tiles fastest: they share the weight columns
+          const int rt = tile_off[lo + 1] - tile_off[lo], j = i - tile_off[lo] * MT;
+          const int mb = j / rt, r = j - mb * rt;
+          const int rows = goff[lo + 1] - goff[lo], per = mx4_rows_per_tile(rows, rt);
+          t.g = lo;
+          t.m0 = mb * kMx4BM;
+          t.r0 = goff[lo] + r * per;
+          t.rows = min(per, rows - r * per);
+          t.n = (t.rows + 15) / 16 * 16;
+          t.xt = min(tile_off[lo] + r, args.row_tiles - 1);
+        }
+        const int q = n % kMx4Sched;
+        if (!mbar_wait(&rempty[q], ((n / kMx4Sched) & 1) ^ 1, abort_flag, lim)) { ok = false; break; }
+        ring[q] = t;
+        mbar_arrive(&rfull[q]);
+        if (i >= total) break;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(DEVERR_TIMEOUT);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ producer of the codes (both CTAs)
+    if (lane == 0) {
+      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
-        const TileInfo ti = decode_tile(i, tile_off, goff, G, NT, kMx4TN);
-        const int rba = min(tile_off[ti.g] + (ti.m0 - goff[ti.g]) / kBM, args.row_blocks - 1);
-        const int rbw = ti.n0 / kBM;
-        const int nrb = min(2, NBW - rbw);
-        const uint8_t* sa = args.tiles_a + rba * row_block;
-        const uint8_t* sw = args.tiles_w + (static_cast<size_t>(ti.g) * NBW + rbw) * row_block;
-        const uint32_t tx = LY::A_BYTES + LY::B_BYTES + LY::SFA_BYTES + nrb * 1024u;
+      Mx4Tile ti;
+      for (int n = 0;; ++n) {
+        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (ti.g < 0) break;
+        const int q32 = (ti.n + 63) / 64;                  // boxes of 32 rows in half of the rows
+        const CUtensorMap* tx = &args.x[q32 - 1];
+        const int row = ti.r0 + rank * (ti.n / 2), col = ti.m0 + rank * 128;
+        const uint32_t bytes = 2u * (LY::A_BYTES + q32 * 32 * 128 + LY::SFA_BYTES + LY::SFB_BYTES);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[s], tx);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           uint8_t* st = smem + s * LY::STAGE_BYTES;
-          tma_load_3d(st + LY::A_BYTES, &tmB, &full[s], kb * 128, ti.n0, ti.g);
-          tma_load_2d(st, &tmA, &full[s], kb * 128, ti.m0);
-          uint8_t* sf = st + LY::A_BYTES + LY::B_BYTES;
-          bulk_load(sf, sa + kb * 1024, 1024, &full[s]);
-          for (int q = 0; q < nrb; ++q) bulk_load(sf + 1024 * (1 + q), sw + q * row_block + kb * 1024, 1024, &full[s]);
+          const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
+          tma_load_3d_pair(st, &args.w, fb, kb * 128, col, ti.g);
+          tma_load_2d_pair(st + LY::A_BYTES, tx, fb, kb * 128, row);
           issued |= 1u << s;
           issued_par = (issued_par & ~(1u << s)) | (ph << s);
           if (++s == kMx4Stages) { s = 0; ph ^= 1u; }
         }
+        if (!ok) break;
       }
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
+        // the peer's barrier cannot be polled from here: give loads in flight time to land
+        for (int q = 0; q < 2000; ++q) __nanosleep(1000);
       }
-      for (int q = 0; q < kMx4Stages; ++q)
-        if ((issued >> q) & 1u)
-          if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+      if (rank == 0)
+        for (int q = 0; q < kMx4Stages; ++q)
+          if ((issued >> q) & 1u)
+            if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ producer of the scales (both CTAs)
+    if (lane == 0) {
+      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      const int NBW = (args.n_out + 127) / 128;
+      int s = 0;
+      uint32_t ph = 0;
+      Mx4Tile ti;
+      for (int n = 0;; ++n) {
+        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (ti.g < 0) break;
+        // the pair's second block may lie behind the last one: its columns are not stored
+        const int wrow = (ti.g * NBW + min(ti.m0 / 128 + rank, NBW - 1)) * KB * (LY::SFA_BYTES / 256);
+        const int xrow = ti.xt * KB * (LY::SFB_BYTES / 256);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
+          uint8_t* sf = smem + s * LY::STAGE_BYTES + LY::A_BYTES + LY::B_BYTES;
+          const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
+          tma_load_2d_pair(sf, &args.sw, fb, 0, wrow + kb * (LY::SFA_BYTES / 256));
+          tma_load_2d_pair(sf + LY::SFA_BYTES, &args.sx, fb, 0, xrow + kb * (LY::SFB_BYTES / 256));
+          if (++s == kMx4Stages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(DEVERR_TIMEOUT);
+        for (int q = 0; q < 2000; ++q) __nanosleep(1000);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int s = 0, it = 0;
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    // The whole warp walks the stages, so that addresses and descriptors are uniform values
+    // the tensor instructions take as they are; one elected lane issues them.  (One lane
+    // walking alone moves every operand over: 830 cycles a stage for 460 of instructions.)
+    if (rank == 0) {
+      const uint32_t s_addr = smem_u32(smem);
+      const uint64_t a_desc = sw128_kmajor_desc(s_addr), b_desc = sw128_kmajor_desc(s_addr + LY::A_BYTES);
+      const uint64_t sf_desc = sf_chunk_desc(s_addr + LY::A_BYTES + LY::B_BYTES);
+      const bool leader = elect_one();
+      int s = 0;
       uint32_t ph = 0, par = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; ok && i < total; i += gridDim.x, ++it) {
-        const TileInfo ti = decode_tile(i, tile_off, goff, G, NT, kMx4TN);
-        const int acc = it & 1;
-        if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+      bool issued_any = false;
+      Mx4Tile ti;
+      for (int n = 0;; ++n) {
+        if (!next_tile(n, ti, true)) { ok = false; break; }
+        if (__shfl_sync(0xffffffffu, ti.g, 0) < 0) break;
+        const int tn = __shfl_sync(0xffffffffu, ti.n, 0);
+        const int acc = n & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim))) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
-        const uint32_t half = (ti.n0 & 127) != 0 ? 2u : 0u;   // the tile starts 64 rows into a chunk
+        const uint32_t idesc = make_idesc_mx4(kMx4BM, tn, 0);
+        constexpr uint32_t kSfId2 = (2u << 4) | (2u << 29);
+        const bool two = tn > 128;                         // the rows' scales take two chunks
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&full[s], ph, abort_flag, lim)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, lim))) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + s * LY::STAGE_BYTES);
-          const uint32_t b_addr = a_addr + LY::A_BYTES;
-          const uint32_t sf_addr = b_addr + LY::B_BYTES;
-          // scales of even and odd stages sit in different columns: a stage's copy need not
+          const uint64_t so = static_cast<uint64_t>(s * (LY::STAGE_BYTES >> 4));
+          const uint64_t ad = a_desc + so, bd = b_desc + so, fd = sf_desc + so;
+          // scales of even and odd stages sit in different columns: a stage's copies need not
           // wait for the MMAs of the stage before it to have read theirs
           const uint32_t sf = tmem_base + static_cast<uint32_t>(LY::SF_COL) + par * kAccStride;
+          if (leader) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tc_cp_sf(sf + 4 * c, sf_chunk_desc(sf_addr + 512 * c));
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              tc_cp_sf(sf + LY::SFB_COL + 8 * c + 4 * q, sf_chunk_desc(sf_addr + 1024 * (1 + q) + 512 * c));
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const uint32_t sel = static_cast<uint32_t>(2 * kk) << 30;
-              tc_mma_mx4(d_tmem, sw128_kmajor_desc(a_addr + c * 64 + kk * 32),
-                         sw128_kmajor_desc(b_addr + c * 64 + kk * 32), make_idesc_mx4(kBM, kMx4TN, 2 * kk),
-                         (sf + 4 * c) | sel, (sf + LY::SFB_COL + 8 * c + half) | sel, (kb | c | kk) != 0 ? 1u : 0u);
+            for (int c = 0; c < 2; ++c) {
+              tc_cp_sf_pair(sf + 4 * c, fd + c * (512 >> 4));
+              tc_cp_sf_pair(sf + LY::SFB_COL + 8 * c, fd + ((LY::SFA_BYTES + 1024 * c) >> 4));
+              if (two) tc_cp_sf_pair(sf + LY::SFB_COL + 8 * c + 4, fd + ((LY::SFA_BYTES + 1024 * c + 512) >> 4));
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {                  // K = 64 each: chunk q / 2, byte pair q % 2
+              const uint32_t sel = static_cast<uint32_t>(2 * (q & 1)) << 30;
+              tc_mma_mx4_pair(d_tmem, ad + q * 2, bd + q * 2, (q & 1) ? (idesc | kSfId2) : idesc,
+                              (sf + 4 * (q >> 1)) | sel, (sf + LY::SFB_COL + 8 * (q >> 1)) | sel,
+                              (kb | q) != 0 ? 1u : 0u);
+            }
+            tc_commit_pair_mc(&empty[s], 0x3);
           }
-          tc_commit(&empty[s]);
+          __syncwarp();
+          issued_any = true;
           par ^= 1u;
           if (++s == kMx4Stages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        tc_commit(&tfull[acc]);
+        if (leader) tc_commit_pair_mc(&tfull[acc], 0x3);
+        __syncwarp();
       }
-      if (!ok) {
-        *abort_flag = 1;
-        flag_error(DEVERR_TIMEOUT);
+      if (leader) {
+        if (!ok) {
+          *abort_flag = 1;
+          flag_error(DEVERR_TIMEOUT);
+        }
+        if (issued_any) {
+          tc_commit_pair(drain);
+          if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+        }
       }
-      tc_commit(drain);
-      if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5)
-    constexpr int COLS = 128 / static_cast<int>(sizeof(OutT));
-    const int quarter = warp & 3;
-    uint8_t* stage = staging + quarter * (32 * 144);
-    int it = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; i < total; i += gridDim.x, ++it) {
-      const TileInfo ti = decode_tile(i, tile_off, goff, G, NT, kMx4TN);
-      const int acc = it & 1;
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], (it >> 1) & 1, abort_flag, lim));
-      if (!got) { ok = false; break; }
-      tc_fence_after();
+    // ------------------------------------------------------------ epilogue (warps 2..9)
+    // Lane = output column, accumulator column = row: each store of the warp is one run of a
+    // row.  Two warps share a TMEM lane quarter and take 16 rows in turn.
+    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    Mx4Tile ti;
+    for (int n = 0;; ++n) {
+      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (ti.g < 0) break;
+      const int acc = n & 1;
+      const int col = ti.m0 + rank * 128 + quarter * 32 + lane;
+      const int rows = col < args.n_out ? ti.rows : 0;
+      float bias = 0.0f;
+      if (args.bias != nullptr && col < args.n_out)
+        bias = __bfloat162float(args.bias[static_cast<size_t>(ti.g) * args.n_out + col]);
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kAccStride);
-      const int row0 = ti.m0 + quarter * 32;
-      OutT* out = static_cast<OutT*>(args.out) + static_cast<size_t>(row0) * args.n_out + ti.n0;
-      const __nv_bfloat16* bias =
-          args.bias == nullptr ? nullptr : args.bias + static_cast<size_t>(ti.g) * args.n_out + ti.n0;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
+      tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < kMx4TN; c += COLS) {
-        const int left = args.n_out - ti.n0 - c;
-        if (left <= 0) break;
-        float v[COLS];
-#pragma unroll
-        for (int j = 0; j < COLS; j += 8) tmem_ld8(tbase + c + j, *reinterpret_cast<float(*)[8]>(v + j));
+      for (int c = 16 * half; c < ti.rows; c += 32) {
+        float v[16];
+        tmem_ld8(tbase + c, *reinterpret_cast<float(*)[8]>(v));
+        tmem_ld8(tbase + c + 8, *reinterpret_cast<float(*)[8]>(v + 8));
         tmem_ld_wait();
-        if (bias != nullptr) {
+        OutT* o = static_cast<OutT*>(args.out) + static_cast<size_t>(ti.r0 + c) * args.n_out + col;
 #pragma unroll
-          for (int j = 0; j < COLS; j += 8)
-            if (j < left) {
-              float b[8];
-              load8<__nv_bfloat16>(bias + c + j, b);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) v[j + q] += b[q];
-            }
-        }
-        store_rows_staged<OutT>(stage, out + c, args.n_out, ti.m_end - row0, left, v);
+        for (int j = 0; j < 16; ++j, o += args.n_out)
+          if (c + j < rows) {
+            if constexpr (sizeof(OutT) == 2) *o = __float2bfloat16_rn(v[j] + bias);
+            else *o = v[j] + bias;
+          }
       }
       tc_fence_before();
-      mbar_arrive(&tempty[acc]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc) * 8u);
     }
     if (!ok) {
       *abort_flag = 1;
@@ -317,9 +411,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();   // no CTA leaves while its peer may still signal it or read its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, kTmemCols);
   }
 }
 

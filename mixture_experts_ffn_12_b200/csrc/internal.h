@@ -130,7 +130,8 @@ cudaError_t mx4_quant_rows(const Launch& L, bool bf16, int64_t rows, int K, cons
 cudaError_t mx4_dequant_rows(const Launch& L, bool bf16, int64_t rows, int K, const uint8_t* codes,
                              const uint8_t* scales, void* out);
 cudaError_t mx4_scale_tiles(const Launch& L, int G, int N, int K, const uint8_t* scales, uint8_t* tiles);
-int64_t mx4_row_blocks(int64_t R, int G);
+int64_t mx4_row_tiles(int64_t R, int G);
+size_t mx4_row_tiles_bytes(int64_t R, int G, int K);
 cudaError_t mx4_quant_tiles(const Launch& L, int64_t R, int K, const void* x, const int32_t* off, int G,
                             uint8_t* codes, uint8_t* tiles);
 // out [R, N] (bf16, or fp32 if out_f32) = A W_g^T + bias_g; off null: one group; bias may be null.

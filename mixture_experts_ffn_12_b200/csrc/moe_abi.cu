@@ -404,7 +404,7 @@ struct LinearLayout {
 LinearLayout linear_layout(int32_t G, int64_t R, int32_t K) {
   LinearLayout L{};
   L.tiles = align256(size_t(R) * (K / 2));
-  L.total = L.tiles + size_t(moe::mx4_row_blocks(R, G)) * moe::mx4_chunks(K) * 512;
+  L.total = L.tiles + moe::mx4_row_tiles_bytes(R, G, K);
   return L;
 }
 

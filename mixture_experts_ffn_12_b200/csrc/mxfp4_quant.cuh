@@ -13,13 +13,15 @@
 // of a warp is contiguous, and the block maximum takes two shuffles.
 //
 // Scale layouts.  "Rows": [rows, K/32], what the MXFP4 expert weights of the layer use.
-// "Tiles": what the 4-bit x 4-bit product reads: for every 128 rows (counted from the
-// start of a group of rows) and every 128 elements of K one 512-byte chunk, in which
-// byte 16 (r % 32) + 4 (r % 128 / 32) + b holds row r's scale of block b = 0..3 -- the
-// 32-lane x 16-byte image that tcgen05.cp copies to TMEM.  The chunks of a row block are
-// consecutive along K and padded to an even number (one pipeline stage of the product
-// covers 256 elements); padding along K holds 127 (2^0: it scales codes that read as
-// zero), padding rows are never used.
+// "Tiles": what the 4-bit x 4-bit product reads: for 128 rows and 128 elements of K one
+// 512-byte chunk, in which byte 16 (r % 32) + 4 (r / 32) + b holds row r's scale of block
+// b = 0..3 -- the 32-lane x 16-byte image that tcgen05.cp copies to TMEM.  Padding along K
+// holds 127 (2^0: it scales codes that read as zero), padding rows are never used.
+//   Weights: row blocks of 128 within each group, a block's chunks one after another along
+//   K, an even number of them (a pipeline stage of the product covers 256 elements).
+//   Activations: a group's rows split evenly into tiles of at most 192 (mx4_rows_per_tile,
+//   the product's N), for each tile and 256 elements of K 2 x 2 chunks: of the tile's rows
+//   below and above 128 for the first 128 elements, then for the others.
 #pragma once
 
 #include "grouped_gemm_mx8.cuh"
@@ -28,6 +30,13 @@ namespace moe {
 
 // 128-element chunks of a scale tile row, an even number.
 __host__ __device__ constexpr int mx4_chunks(int K) { return 2 * ((K + 255) / 256); }
+
+// Rows of the product's tiles: a group's rows in `tiles` = ceil(rows / kMx4Rows) even parts,
+// a multiple of 16 each (never above kMx4Rows, never leaving a tile without rows).
+constexpr int kMx4Rows = 192;
+__host__ __device__ constexpr int mx4_rows_per_tile(int rows, int tiles) {
+  return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+}
 
 // The block scale exponent from the largest |x| as fp32 bits (finite): 6 = 1.5 * 2^2.
 __device__ __forceinline__ int mx4_exponent(uint32_t amax_bits) {
@@ -133,43 +142,72 @@ __device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int r
 }
 
 // x [rows, K] bf16, rows grouped by off (null: one group) -> codes [rows, K/2] and scale
-// tiles, the row blocks counted group after group.  Rows outside every group are skipped.
+// tiles, the row tiles counted group after group.  Rows outside every group are skipped.
+// A warp takes up to kMx4QuantSpan elements of a row (all loads in flight before the first
+// is used); the row's place in the tiles is looked up once, and the scales of 128 elements
+// (four blocks, 16 lanes) leave as one 4-byte word.
+constexpr int kMx4QuantSpan = 1024;
 __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, int rows, int K,
-                                                              const int32_t* __restrict__ off, int G, int max_blocks,
+                                                              const int32_t* __restrict__ off, int G, int max_tiles,
                                                               uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ tiles) {
   pdl_enter();
   __shared__ int goff[kMaxGroups + 2];
-  __shared__ int blk[kMaxGroups + 2];
-  if (threadIdx.x < 32) mx4_group_table(off, G, rows, goff, blk);
+  __shared__ int tile_off[kMaxGroups + 2];
+  if (threadIdx.x < 32) mx4_group_table<kMx4Rows>(off, G, rows, goff, tile_off);
   __syncthreads();
-  const int nb = K / 32, kc = mx4_chunks(K);
-  const int64_t total = static_cast<int64_t>(rows) * nb * 4;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < total; i += step) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (i < total) load8<__nv_bfloat16>(x + i * 8, v);
-    uint32_t s;
-    const uint32_t q = mx4_quantize8(v, s);
-    if (i >= total) continue;
-    const int64_t b = i >> 2;
-    const int row = static_cast<int>(b / nb);
-    const int kb = static_cast<int>(b - static_cast<int64_t>(row) * nb);
-    codes[i] = q;
-    if ((i & 3) != 0) continue;
+  const int lane = threadIdx.x & 31;
+  const int kc = mx4_chunks(K);
+  const int spans = (K + kMx4QuantSpan - 1) / kMx4QuantSpan;
+  const int64_t total = static_cast<int64_t>(rows) * spans;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  constexpr int IT = kMx4QuantSpan / 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < total; i += step) {
+    const int row = static_cast<int>(i / spans);
+    const int k0 = static_cast<int>(i - static_cast<int64_t>(row) * spans) * kMx4QuantSpan + lane * 8;
+    const __nv_bfloat16* src = x + static_cast<size_t>(row) * K;
+    uint4 raw[IT];
+#pragma unroll
+    for (int t = 0; t < IT; ++t)
+      raw[t] = k0 + 256 * t < K ? *reinterpret_cast<const uint4*>(src + k0 + 256 * t) : make_uint4(0, 0, 0, 0);
     int lo = 0, hi = G;   // goff[lo] <= row < goff[hi] where the row is in a group
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (goff[mid] <= row) lo = mid; else hi = mid;
     }
-    if (row < goff[lo] || row >= goff[lo + 1]) continue;
-    const int p = row - goff[lo];
-    const int rb = blk[lo] + p / kBM;
-    if (rb >= max_blocks) continue;   // offsets that are not ascending (flagged)
-    uint8_t* t = tiles + (static_cast<size_t>(rb) * kc) * 512 + 16 * (p & 31) + 4 * ((p & 127) >> 5);
-    t[static_cast<size_t>(kb >> 2) * 512 + (kb & 3)] = static_cast<uint8_t>(s);
-    if (kb == nb - 1)
-      for (int c = nb; c < 4 * kc; ++c) t[static_cast<size_t>(c >> 2) * 512 + (c & 3)] = 127;
+    const int grows = goff[lo + 1] - goff[lo], rt = tile_off[lo + 1] - tile_off[lo];
+    int p = row - goff[lo], tile = 0;
+    bool in = p >= 0 && p < grows;
+    if (in) {
+      const int per = mx4_rows_per_tile(grows, rt);
+      tile = p / per;
+      p -= tile * per;
+      tile += tile_off[lo];
+      in = tile < max_tiles;   // offsets that are not ascending (flagged)
+    }
+    uint8_t* dst = tiles + static_cast<size_t>(tile) * kc * 1024 + 512 * (p >> 7) + 16 * (p & 31) + 4 * ((p & 127) >> 5);
+#pragma unroll
+    for (int t = 0; t < IT; ++t) {
+      const int k = k0 + 256 * t;
+      float v[8];
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw[t]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __bfloat1622float2(h[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+      uint32_t s;
+      const uint32_t q = mx4_quantize8(v, s);
+      if (k < K) codes[(static_cast<size_t>(row) * K + k) >> 3] = q;
+      // lanes 0, 4, 8, 12 of each half warp hold the scales of a chunk's four blocks
+      if (k >= K) s = 127;
+      uint32_t w = s << (8 * ((lane >> 2) & 3));
+      w |= __shfl_xor_sync(0xffffffffu, w, 4);
+      w |= __shfl_xor_sync(0xffffffffu, w, 8);
+      const int c = k >> 7;
+      if (in && (lane & 15) == 0 && c < kc) *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(c) * 1024) = w;
+    }
   }
 }
 
@@ -263,14 +301,18 @@ cudaError_t mx4_scale_tiles(const Launch& L, int G, int N, int K, const uint8_t*
   return cudaGetLastError();
 }
 
-// Row blocks that R rows in G groups can take: every group may end in a partial one.
-int64_t mx4_row_blocks(int64_t R, int G) { return (R + kBM - 1) / kBM + std::min<int64_t>(G - 1, R); }
+// Row tiles that R rows in G groups can take: every group may end in a partial one.
+int64_t mx4_row_tiles(int64_t R, int G) { return (R + kMx4Rows - 1) / kMx4Rows + std::min<int64_t>(G - 1, R); }
+size_t mx4_row_tiles_bytes(int64_t R, int G, int K) {
+  return static_cast<size_t>(mx4_row_tiles(R, G)) * mx4_chunks(K) * 1024;
+}
 
 cudaError_t mx4_quant_tiles(const Launch& L, int64_t R, int K, const void* x, const int32_t* off, int G,
                             uint8_t* codes, uint8_t* tiles) {
-  pdl_launch(mx4_quant_tiles_kernel, dim3(mx4_blocks(L, R * (K / 8))), dim3(256), 0, L.stream,
+  const int64_t warps = R * ((K + kMx4QuantSpan - 1) / kMx4QuantSpan);
+  pdl_launch(mx4_quant_tiles_kernel, dim3(mx4_blocks(L, warps * 32)), dim3(256), 0, L.stream,
              static_cast<const __nv_bfloat16*>(x), static_cast<int>(R), K, off, G,
-             static_cast<int>(mx4_row_blocks(R, G)), reinterpret_cast<uint32_t*>(codes), tiles);
+             static_cast<int>(mx4_row_tiles(R, G)), reinterpret_cast<uint32_t*>(codes), tiles);
   count_launch();
   return cudaGetLastError();
 }

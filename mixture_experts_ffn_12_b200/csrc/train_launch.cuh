@@ -61,14 +61,27 @@ static cudaError_t make_bwd_maps(BwdMaps* m, const void* ptr, uint64_t cols, uin
 // ---------------------------------------------------------------------------
 // MXFP4 product
 // ---------------------------------------------------------------------------
+// Runs of bytes as rows of 256 B; boxes of box_rows of them, no swizzle.
+static cudaError_t make_tmap_runs(CUtensorMap* m, const void* ptr, uint64_t bytes, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {256, bytes / 256};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {256, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename OutT>
-static cudaError_t launch_mx4(const Launch& L, const CUtensorMap& a, const CUtensorMap& b, const Mx4Args& args,
-                              int64_t max_tiles) {
-  auto kern = grouped_gemm_mx4_kernel<OutT>;
+static cudaError_t launch_mx4(const Launch& L, const Mx4Args& args, int64_t max_tiles) {
   const cudaError_t e = allow_smem<grouped_gemm_mx4_kernel<OutT>>(Mx4Layout::SMEM);
   if (e != cudaSuccess) return e;
-  pdl_launch(kern, dim3(static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms))), dim3(kGemmThreads),
-             Mx4Layout::SMEM, L.stream, a, b, args);
+  auto kern = grouped_gemm_mx4_kernel<OutT>;   // clusters of two CTAs
+  pdl_launch(kern, dim3(2 * static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms / 2))), dim3(kMx4Threads),
+             Mx4Layout::SMEM, L.stream, args);
   count_launch();
   return cudaGetLastError();
 }
@@ -76,24 +89,25 @@ static cudaError_t launch_mx4(const Launch& L, const CUtensorMap& a, const CUten
 cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const uint8_t* codes, const uint8_t* tiles,
                         const int32_t* off, const uint8_t* w_codes, const uint8_t* w_tiles, const void* bias,
                         bool out_f32, void* out) {
-  CUtensorMap ta, tb;
-  cudaError_t e;
-  if ((e = make_tmap_bytes(&ta, codes, K / 2, R, 0, kBM)) != cudaSuccess) return e;
-  if ((e = make_tmap_bytes(&tb, w_codes, K / 2, N, G, kMx4TN)) != cudaSuccess) return e;
   Mx4Args a{};
+  cudaError_t e;
+  if ((e = make_tmap_bytes(&a.w, w_codes, K / 2, N, G, 128)) != cudaSuccess) return e;
+  for (int q = 0; q < 3; ++q)
+    if ((e = make_tmap_bytes(&a.x[q], codes, K / 2, R, 0, 32 * (q + 1))) != cudaSuccess) return e;
+  const uint64_t wt = static_cast<uint64_t>(G) * ((N + 127) / 128) * mx4_chunks(K) * 512;
+  if ((e = make_tmap_runs(&a.sw, w_tiles, wt, 4)) != cudaSuccess) return e;
+  if ((e = make_tmap_runs(&a.sx, tiles, mx4_row_tiles_bytes(R, G, K), 8)) != cudaSuccess) return e;
   a.group_off = off;
   a.num_groups = G;
   a.m_total = static_cast<int>(R);
   a.n_out = N;
   a.k_dim = K;
-  a.tiles_a = tiles;
-  a.row_blocks = static_cast<int>(mx4_row_blocks(R, G));
-  a.tiles_w = w_tiles;
+  a.row_tiles = static_cast<int>(mx4_row_tiles(R, G));
   a.bias = static_cast<const __nv_bfloat16*>(bias);
   a.out = out;
   a.wait_limit_ns = L.wait_limit_ns;
-  const int64_t max_tiles = mx4_row_blocks(R, G) * ((N + kMx4TN - 1) / kMx4TN);
-  return out_f32 ? launch_mx4<float>(L, ta, tb, a, max_tiles) : launch_mx4<__nv_bfloat16>(L, ta, tb, a, max_tiles);
+  const int64_t max_tiles = mx4_row_tiles(R, G) * ((N + kMx4BM - 1) / kMx4BM);
+  return out_f32 ? launch_mx4<float>(L, a, max_tiles) : launch_mx4<__nv_bfloat16>(L, a, max_tiles);
 }
 
 // ---------------------------------------------------------------------------
