@@ -16,9 +16,7 @@
 // the mxf4 MMA reads 4-bit operands packed); the scales come as ready-made 512-byte chunks
 // (mxfp4_quant.cuh) by TMA, tcgen05.cp brings them to TMEM, four MMAs of K = 64.
 //
-// Roles (384 threads a CTA): warp 0 producer of the codes, warp 11 of the scales (a copy
-// instruction costs a thread some 100 cycles, a stage has four and 384 cycles of MMAs);
-// warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue; warp 10 the tile
+// Roles (384 threads a CTA): warp 0 producer of the codes, warp 11 of the scales; warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue; warp 10 the tile
 // scheduler.  Waits bounded and the closing cluster barrier as in grouped_gemm_pair.cuh.
 #pragma once
 
@@ -71,17 +69,6 @@ __device__ __forceinline__ void tc_mma_mx4_pair(uint32_t d_tmem, uint64_t adesc,
 // tc_cp_sf in both CTAs of the pair, each from its own shared memory to its own TMEM.
 __device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
-// One lane of a converged warp (the same one every time).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
 }
 
 struct Mx4Args {
@@ -186,6 +173,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     if (!whole_warp || lane == 0) mbar_arrive(&rempty[q]);
     return true;
   };
+  // A tile that the whole warp has read, as values the compiler knows to be the same in every lane.
+  auto uniform = [](Mx4Tile& t) {
+    t.g = __shfl_sync(0xffffffffu, t.g, 0);
+    t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);
+    t.r0 = __shfl_sync(0xffffffffu, t.r0, 0);
+    t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+    t.n = __shfl_sync(0xffffffffu, t.n, 0);
+    t.xt = __shfl_sync(0xffffffffu, t.xt, 0);
+  };
   bool ok = true;
 
   if (warp == 10) {
@@ -227,25 +223,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     __syncwarp();
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer of the codes (both CTAs)
-    if (lane == 0) {
+    {
+      const bool leader = elect_one();
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;
       Mx4Tile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (!next_tile(n, ti, true)) { ok = false; break; }
+        uniform(ti);
         if (ti.g < 0) break;
         const int q32 = (ti.n + 63) / 64;                  // boxes of 32 rows in half of the rows
         const CUtensorMap* tx = &args.x[q32 - 1];
         const int row = ti.r0 + rank * (ti.n / 2), col = ti.m0 + rank * 128;
         const uint32_t bytes = 2u * (LY::A_BYTES + q32 * 32 * 128 + LY::SFA_BYTES + LY::SFB_BYTES);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim))) { ok = false; break; }
           uint8_t* st = smem + s * LY::STAGE_BYTES;
           const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
-          tma_load_3d_pair(st, &args.w, fb, kb * 128, col, ti.g);
-          tma_load_2d_pair(st + LY::A_BYTES, tx, fb, kb * 128, row);
+          if (leader) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+            tma_load_3d_pair(st, &args.w, fb, kb * 128, col, ti.g);
+            tma_load_2d_pair(st + LY::A_BYTES, tx, fb, kb * 128, row);
+          }
+          __syncwarp();
           issued |= 1u << s;
           issued_par = (issued_par & ~(1u << s)) | (ph << s);
           if (++s == kMx4Stages) { s = 0; ph ^= 1u; }
@@ -258,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
         // the peer's barrier cannot be polled from here: give loads in flight time to land
         for (int q = 0; q < 2000; ++q) __nanosleep(1000);
       }
-      if (rank == 0)
+      if (leader && rank == 0)
         for (int q = 0; q < kMx4Stages; ++q)
           if ((issued >> q) & 1u)
             if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
@@ -266,24 +267,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------------------ producer of the scales (both CTAs)
-    if (lane == 0) {
+    {
+      const bool leader = elect_one();
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       const int NBW = (args.n_out + 127) / 128;
       int s = 0;
       uint32_t ph = 0;
       Mx4Tile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (!next_tile(n, ti, true)) { ok = false; break; }
+        uniform(ti);
         if (ti.g < 0) break;
         // the pair's second block may lie behind the last one: its columns are not stored
         const int wrow = (ti.g * NBW + min(ti.m0 / 128 + rank, NBW - 1)) * KB * (LY::SFA_BYTES / 256);
         const int xrow = ti.xt * KB * (LY::SFB_BYTES / 256);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim))) { ok = false; break; }
           uint8_t* sf = smem + s * LY::STAGE_BYTES + LY::A_BYTES + LY::B_BYTES;
           const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
-          tma_load_2d_pair(sf, &args.sw, fb, 0, wrow + kb * (LY::SFA_BYTES / 256));
-          tma_load_2d_pair(sf + LY::SFA_BYTES, &args.sx, fb, 0, xrow + kb * (LY::SFB_BYTES / 256));
+          if (leader) {
+            tma_load_2d_pair(sf, &args.sw, fb, 0, wrow + kb * (LY::SFA_BYTES / 256));
+            tma_load_2d_pair(sf + LY::SFA_BYTES, &args.sx, fb, 0, xrow + kb * (LY::SFB_BYTES / 256));
+          }
+          __syncwarp();
           if (++s == kMx4Stages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
@@ -311,15 +317,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
       Mx4Tile ti;
       for (int n = 0;; ++n) {
         if (!next_tile(n, ti, true)) { ok = false; break; }
-        if (__shfl_sync(0xffffffffu, ti.g, 0) < 0) break;
-        const int tn = __shfl_sync(0xffffffffu, ti.n, 0);
+        uniform(ti);
+        if (ti.g < 0) break;
         const int acc = n & 1;
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim))) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
-        const uint32_t idesc = make_idesc_mx4(kMx4BM, tn, 0);
+        const uint32_t idesc = make_idesc_mx4(kMx4BM, ti.n, 0);
         constexpr uint32_t kSfId2 = (2u << 4) | (2u << 29);
-        const bool two = tn > 128;                         // the rows' scales take two chunks
+        const bool two = ti.n > 128;                       // the rows' scales take two chunks
         for (int kb = 0; kb < KB; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, lim))) { ok = false; break; }
           tc_fence_after();
@@ -392,12 +398,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
         tmem_ld8(tbase + c + 8, *reinterpret_cast<float(*)[8]>(v + 8));
         tmem_ld_wait();
         OutT* o = static_cast<OutT*>(args.out) + static_cast<size_t>(ti.r0 + c) * args.n_out + col;
+        if constexpr (sizeof(OutT) == 2) {
+          // neighbouring lanes trade, so that one has both columns of row j, the other of row
+          // j + 1: a store of four bytes a lane covers 64 bytes of two rows
+          o += (lane & 1) * (args.n_out - 1);
 #pragma unroll
-        for (int j = 0; j < 16; ++j, o += args.n_out)
-          if (c + j < rows) {
-            if constexpr (sizeof(OutT) == 2) *o = __float2bfloat16_rn(v[j] + bias);
-            else *o = v[j] + bias;
+          for (int j = 0; j < 16; j += 2, o += 2 * static_cast<size_t>(args.n_out)) {
+            const __nv_bfloat162 mine = __floats2bfloat162_rn(v[j] + bias, v[j + 1] + bias);
+            const uint32_t a = *reinterpret_cast<const uint32_t*>(&mine);
+            const uint32_t b = __shfl_xor_sync(0xffffffffu, a, 1);
+            const uint32_t both = (lane & 1) ? __byte_perm(b, a, 0x7632) : __byte_perm(a, b, 0x5410);
+            if (c + j + (lane & 1) < rows) *reinterpret_cast<uint32_t*>(o) = both;
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, o += args.n_out)
+            if (c + j < rows) *o = v[j] + bias;
+        }
       }
       tc_fence_before();
       __syncwarp();
