@@ -339,6 +339,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
     if (!whole_warp || lane == 0) mbar_arrive(&sempty[q]);
     return true;
   };
+  // A tile that the whole warp has read, as values the compiler knows to be the same in every lane.
+  auto uniform = [](BwdTile& t) {
+    int* f = reinterpret_cast<int*>(&t);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(BwdTile) / sizeof(int)); ++i) f[i] = __shfl_sync(0xffffffffu, f[i], 0);
+  };
   bool ok = true;
 
   if (warp == 2 + kBwdEpiWarps) {
@@ -369,13 +375,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    // As in the issuer, the whole warp walks the stages with uniform values and one elected
+    // lane issues the copies.
+    {
+      const bool leader = elect_one();
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;         // stages counted on the leader's full
       uint32_t tails = 0, tail_par = 0, tail_uses = 0;     // stages counted on this CTA's landed
       BwdTile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (!next_tile(n, ti, true)) { ok = false; break; }
+        uniform(ti);
         if (ti.job < 0) break;
         const BwdJob& jb = args.job[ti.job];
         const int a_row = ti.m0 + rank * 128;
@@ -385,48 +395,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
         const int b_row = ti.r0 + rank * (ti.n / 2), q32 = (ti.n + 63) / 64;   // DH, DX: boxes of 32 rows
         const uint32_t tx = LY::A_BYTES + (KIND == BWD_DW ? ti.units * kBwdBox : q32 * (kBwdBox / 2));
         for (int kb = 0; kb < ti.kb; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim))) { ok = false; break; }
           uint8_t* sa = smem + s * LY::STAGE_BYTES;
           uint8_t* sb = sa + LY::A_BYTES;
           const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
           if (KIND == BWD_DW && kb == ti.kb - 1 && bwd_ragged(ti)) {
             // the blanker is told here, and passes the stage on to the leader
             const int r = ti.r0 + kb * kBwdBK;
-            mbar_arrive_expect_tx(&landed[s], tx);
-            if (b_two) tma_load_3d(sb, &jb.bw.two, &landed[s], 0, r, b_col / 64);
-            else
-              for (int q = 0; q < ti.units; ++q) tma_load_2d(sb + q * kBwdBox, &jb.bw.single, &landed[s], b_col + 64 * q, r);
-            if (a_two) tma_load_3d(sa, &jb.a.two, &landed[s], 0, r, a_row / 64);
-            else
-              for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kBwdBox, &jb.a.single, &landed[s], a_row + 64 * q, r);
+            if (leader) {
+              mbar_arrive_expect_tx(&landed[s], tx);
+              if (b_two) tma_load_3d(sb, &jb.bw.two, &landed[s], 0, r, b_col / 64);
+              else
+                for (int q = 0; q < ti.units; ++q) tma_load_2d(sb + q * kBwdBox, &jb.bw.single, &landed[s], b_col + 64 * q, r);
+              if (a_two) tma_load_3d(sa, &jb.a.two, &landed[s], 0, r, a_row / 64);
+              else
+                for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kBwdBox, &jb.a.single, &landed[s], a_row + 64 * q, r);
+            }
             issued &= ~(1u << s);   // its earlier loads have landed, or the slot were not free
             tails |= 1u << s;
             tail_par = (tail_par & ~(1u << s)) | (tail_uses & (1u << s));
             tail_uses ^= 1u << s;
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * tx);
-            else mbar_arrive_cluster(fb);
-            if constexpr (KIND == BWD_DW) {
-              const int r = ti.r0 + kb * kBwdBK;
-              if (b_two) tma_load_3d_pair(sb, &jb.bw.two, fb, 0, r, b_col / 64);
-              else
-                for (int q = 0; q < ti.units; ++q) tma_load_2d_pair(sb + q * kBwdBox, &jb.bw.single, fb, b_col + 64 * q, r);
-              if (a_two) tma_load_3d_pair(sa, &jb.a.two, fb, 0, r, a_row / 64);
-              else
-                for (int q = 0; q < 2; ++q) tma_load_2d_pair(sa + q * kBwdBox, &jb.a.single, fb, a_row + 64 * q, r);
-            } else {
-              const int half = (KIND == BWD_DX && kb >= KB1) ? 1 : 0;
-              const int k0 = (kb - half * KB1) * kBwdBK;
-              const BwdMaps& ma = half ? jb.a2 : jb.a;
-              if (a_two) tma_load_4d_pair(sa, &ma.two, fb, 0, k0, a_row / 64, ti.g);
-              else
-                for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * kBwdBox, &ma.single, fb, a_row + 64 * q, k0, ti.g);
-              if (KIND == BWD_DX) tma_load_3d_pair(sb, &jb.b[q32 - 1], fb, k0, half, b_row);
-              else tma_load_2d_pair(sb, &jb.b[q32 - 1], fb, k0, b_row);
+            if (leader) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * tx);
+              else mbar_arrive_cluster(fb);
+              if constexpr (KIND == BWD_DW) {
+                const int r = ti.r0 + kb * kBwdBK;
+                if (b_two) tma_load_3d_pair(sb, &jb.bw.two, fb, 0, r, b_col / 64);
+                else
+                  for (int q = 0; q < ti.units; ++q) tma_load_2d_pair(sb + q * kBwdBox, &jb.bw.single, fb, b_col + 64 * q, r);
+                if (a_two) tma_load_3d_pair(sa, &jb.a.two, fb, 0, r, a_row / 64);
+                else
+                  for (int q = 0; q < 2; ++q) tma_load_2d_pair(sa + q * kBwdBox, &jb.a.single, fb, a_row + 64 * q, r);
+              } else {
+                const int half = (KIND == BWD_DX && kb >= KB1) ? 1 : 0;
+                const int k0 = (kb - half * KB1) * kBwdBK;
+                const BwdMaps& ma = half ? jb.a2 : jb.a;
+                if (a_two) tma_load_4d_pair(sa, &ma.two, fb, 0, k0, a_row / 64, ti.g);
+                else
+                  for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * kBwdBox, &ma.single, fb, a_row + 64 * q, k0, ti.g);
+                if (KIND == BWD_DX) tma_load_3d_pair(sb, &jb.b[q32 - 1], fb, k0, half, b_row);
+                else tma_load_2d_pair(sb, &jb.b[q32 - 1], fb, k0, b_row);
+              }
             }
             issued |= 1u << s;
             issued_par = (issued_par & ~(1u << s)) | (ph << s);
           }
+          __syncwarp();
           if (++s == kBwdStages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
@@ -437,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
         // the peer's barrier cannot be polled from here: give loads in flight time to land
         for (int q = 0; q < 2000; ++q) __nanosleep(1000);
       }
-      for (int q = 0; q < kBwdStages; ++q) {
+      for (int q = 0; leader && q < kBwdStages; ++q) {
         if (rank == 0 && ((issued >> q) & 1u))
           if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
         if ((tails >> q) & 1u)
@@ -447,9 +462,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader only)
-    // One thread issues every MMA (128 cycles each at 256 columns): descriptors are made
-    // once and stepped by additions (built per MMA they took 264 cycles an MMA).
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the stages, so that addresses and descriptors (made once, stepped
+    // by additions) are uniform values the tensor instructions take as they are; one elected
+    // lane issues them.
+    if (rank == 0) {
+      const bool leader = elect_one();
       const uint32_t s_addr = smem_u32(smem);
       const uint64_t a_desc = sw128_mnmajor_desc(s_addr);
       const uint64_t b_desc = KIND == BWD_DW ? sw128_mnmajor_desc(s_addr + LY::A_BYTES) : sw128_kmajor_desc(s_addr + LY::A_BYTES);
@@ -461,45 +478,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
       bool issued_any = false;
       BwdTile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, false)) { ok = false; break; }
+        if (!next_tile(n, ti, true)) { ok = false; break; }
+        uniform(ti);
         if (ti.job < 0) break;
         const uint32_t idesc = make_idesc(kBwdBM, ti.n, 1u) | (1u << 15) | (KIND == BWD_DW ? 1u << 16 : 0u);
         const bool sums = KIND == BWD_DW && ti.sums != 0;
         const int acc = n & 1;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
-        if (!mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim))) { ok = false; break; }
         tc_fence_after();
         for (int kb = 0; kb < ti.kb; ++kb) {
-          if (!mbar_wait(&full[s], ph, abort_flag, lim)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, lim))) { ok = false; break; }
           tc_fence_after();
           const uint64_t so = static_cast<uint64_t>(s * (LY::STAGE_BYTES >> 4));
           const uint64_t ad = a_desc + so, bd = b_desc + so;
           const int steps = KIND == BWD_DW ? min(kBwdBK / 16, (ti.rows - kb * kBwdBK + 15) / 16) : kBwdBK / 16;
-          if (steps == kBwdBK / 16 && !sums) {
+          if (leader) {
+            if (steps == kBwdBK / 16 && !sums) {
 #pragma unroll
-            for (int kk = 0; kk < kBwdBK / 16; ++kk)
-              tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
-          } else {
-            for (int kk = 0; kk < steps; ++kk) {
-              const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
-              tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate);
-              if (sums) tc_mma_pair(d_tmem + kBwdOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
+              for (int kk = 0; kk < kBwdBK / 16; ++kk)
+                tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
+            } else {
+              for (int kk = 0; kk < steps; ++kk) {
+                const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
+                tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate);
+                if (sums) tc_mma_pair(d_tmem + kBwdOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
+              }
             }
+            tc_commit_pair_mc(&empty[s], 0x3);
           }
+          __syncwarp();
           issued_any = true;
-          tc_commit_pair_mc(&empty[s], 0x3);
           if (++s == kBwdStages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair_mc(&tfull[acc], 0x3);
+        if (leader) tc_commit_pair_mc(&tfull[acc], 0x3);
+        __syncwarp();
       }
-      if (!ok) {
-        *abort_flag = 1;
-        flag_error(DEVERR_TIMEOUT);
-      }
-      if (issued_any) {
-        tc_commit_pair(drain);
-        if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+      if (leader) {
+        if (!ok) {
+          *abort_flag = 1;
+          flag_error(DEVERR_TIMEOUT);
+        }
+        if (issued_any) {
+          tc_commit_pair(drain);
+          if (!mbar_wait(drain, 0, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
+        }
       }
     }
     __syncwarp();
