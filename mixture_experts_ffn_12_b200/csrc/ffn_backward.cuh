@@ -698,118 +698,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// fp32 layers: the same three products in fp32 FMA (no TF32), 64 x 64 tiles
-// ---------------------------------------------------------------------------
-struct SimtBwdArgs {
-  const int32_t* group_off;
-  int num_groups, m_total;
-  int m, n, k;                // DH, DX: n, k;  DW: gradient rows m, columns n
-  const float *a, *b0, *b1;
-  int lda, ldb;               // DW: row strides of A and B0
-  const float* gu;            // DH: [R, 2, F]
-  float limit, alpha, gate_lo;
-  float *out, *bias_out;
-};
-
-template <int KIND>
-__global__ void __launch_bounds__(256) simt_backward_kernel(const SimtBwdArgs p) {
-  pdl_enter();
-  __shared__ float sa[kSimtBK][kSimtBM + 4];
-  __shared__ float sb[kSimtBK][kSimtBN + 4];
-  __shared__ int goff[kMaxGroups + 2];
-  __shared__ int toff[kMaxGroups + 2];
-  const int G = p.num_groups;
-  for (int g = threadIdx.x; g <= G; g += blockDim.x) {
-    const int v = p.group_off[g];
-    if (v < 0 || v > p.m_total) flag_error(DEVERR_BOUNDS);
-    goff[g] = min(max(v, 0), p.m_total);
-  }
-  __syncthreads();
-  const int n0 = blockIdx.x * kSimtBN;
-  int g, m0, m_end, r0 = 0, K = p.k;
-  if constexpr (KIND == BWD_DW) {
-    g = blockIdx.z;
-    m0 = blockIdx.y * kSimtBM;
-    m_end = p.m;
-    r0 = goff[g];
-    K = max(0, goff[g + 1] - r0);
-  } else {
-    if (threadIdx.x == 0) {
-      toff[0] = 0;
-      for (int q = 0; q < G; ++q) toff[q + 1] = toff[q] + max(0, (goff[q + 1] - goff[q] + kSimtBM - 1) / kSimtBM);
-    }
-    __syncthreads();
-    const int mt = blockIdx.y;
-    if (mt >= toff[G]) return;
-    g = 0;
-    while (toff[g + 1] <= mt) ++g;
-    m0 = goff[g] + (mt - toff[g]) * kSimtBM;
-    m_end = goff[g + 1];
-  }
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {}, sum[4] = {};
-  const int KT = KIND == BWD_DX ? 2 * K : K;
-  for (int k0 = 0; k0 < KT; k0 += kSimtBK) {
-    for (int i = threadIdx.x; i < kSimtBM * kSimtBK; i += 256) {
-      if constexpr (KIND == BWD_DW) {
-        const int kk = i / kSimtBM, r = i % kSimtBM, col = k0 + kk;
-        sa[kk][r] = (m0 + r < m_end && col < K) ? p.a[static_cast<size_t>(r0 + col) * p.lda + m0 + r] : 0.0f;
-        sb[kk][r] = (n0 + r < p.n && col < K) ? p.b0[static_cast<size_t>(r0 + col) * p.ldb + n0 + r] : 0.0f;
-      } else {
-        {
-          const int r = i / kSimtBK, kk = i % kSimtBK, row = m0 + r, col = k0 + kk;
-          sa[kk][r] = (row < m_end && col < KT) ? p.a[static_cast<size_t>(row) * KT + col] : 0.0f;
-        }
-        const int kk = i / kSimtBN, c = i % kSimtBN, col = k0 + kk;
-        const bool second = KIND == BWD_DX && col >= K;
-        const float* b = second ? p.b1 : p.b0;
-        const int kr = second ? col - K : col;
-        sb[kk][c] = (n0 + c < p.n && col < KT) ? b[(static_cast<size_t>(g) * K + kr) * p.n + n0 + c] : 0.0f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kSimtBK; ++kk) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = sa[kk][ty * 4 + i];
-        b[i] = sb[kk][tx * 4 + i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (KIND == BWD_DW) sum[i] += a[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-      }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = m0 + ty * 4 + i;
-    if (row >= m_end) continue;
-    const size_t orow = KIND == BWD_DW ? static_cast<size_t>(g) * p.m + row : row;
-    if (KIND == BWD_DW && p.bias_out != nullptr && n0 == 0 && tx == 0) p.bias_out[orow] = sum[i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      if (n >= p.n) continue;
-      if constexpr (KIND == BWD_DH) {
-        const float gv = p.gu[orow * 2 * p.n + n], uv = p.gu[orow * 2 * p.n + p.n + n];
-        const float gc = fminf(fmaxf(gv, p.gate_lo), p.limit), uc = fminf(fmaxf(uv, -p.limit), p.limit);
-        const float s = 1.0f / (1.0f + expf(-p.alpha * gc)), f = gc * s, dh = acc[i][j];
-        p.out[orow * 2 * p.n + n] =
-            (gv >= p.gate_lo && gv <= p.limit) ? dh * uc * (s + p.alpha * f * (1.0f - s)) : 0.0f;
-        p.out[orow * 2 * p.n + p.n + n] = (uv >= -p.limit && uv <= p.limit) ? dh * f : 0.0f;
-      } else {
-        p.out[orow * p.n + n] = acc[i][j];
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
 // combine, backward: dy_perm[row(t, j)] = w[t, j] dy[t], dw[t, j] = dy[t] . y_perm[row(t, j)]
 // ---------------------------------------------------------------------------
 // One CTA a token: dy[t] is read once and meets its k rows.  Bound by memory: (1 + 2 k) D

@@ -144,10 +144,14 @@ cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const u
 struct Activation {
   float limit, alpha, gate_lo;
 };
-// gate/up projections storing gu [R, 2, F] and h [R, F]; w.b_gate / w.b_up may be null.
-cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
+// gate/up projections of a bf16 layer storing gu [R, 2, F] and h [R, F]; w.b_gate / w.b_up may be null.
+cudaError_t expert_gateup_save(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
                                const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
                                void* h);
+// The whole training forward of an fp32 layer; each bias may be null.
+cudaError_t expert_train_f32(const Launch& L, int64_t R, int D, int F, int E, const float* x_perm,
+                             const int32_t* expert_off, const ExpertWeights& w, const Activation& act, float* gu,
+                             float* h, float* y_perm);
 struct ExpertGrads {
   void *w_gate, *w_up, *w_down, *b_gate, *b_up, *b_down;   // each may be null
 };

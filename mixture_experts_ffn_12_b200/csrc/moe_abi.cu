@@ -895,19 +895,22 @@ moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t 
   const int D = cfg->hidden_size, F = cfg->intermediate_size, E = cfg->num_local_experts;
   const int64_t R = T * cfg->num_experts_per_tok;
   moe::ExpertWeights w = to_internal(weights);
+  const moe::Activation a = activation(cfg, act);
+  const size_t need = align256(size_t(E) * D * elem_size(cfg));
+  const bool zeros = bf16 && weights->b_down == nullptr;   // the down projection's epilogue reads a bias
+  if (zeros && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   Launch L;
-  if (weights->b_down == nullptr) {   // the down projection's epilogue reads a bias: zeros
-    const size_t need = align256(size_t(E) * D * elem_size(cfg));
-    if (ws == nullptr || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
-    if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
+  if (!bf16)
+    return cuda_status(moe::expert_train_f32(L, R, D, F, E, static_cast<const float*>(x_perm), expert_off, w, a,
+                                             static_cast<float*>(gu), static_cast<float*>(h),
+                                             static_cast<float*>(y_perm)));
+  if (zeros) {
     if (cudaMemsetAsync(ws, 0, need, L.stream) != cudaSuccess) return MOE_ERR_CUDA;
     w.b_down = ws;
-  } else if (!get_launch(stream, &L)) {
-    return MOE_ERR_CUDA;
   }
-  if (moe::expert_gateup_save(L, bf16, R, D, F, E, x_perm, expert_off, w, activation(cfg, act), gu, h) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return cuda_status(moe::expert_down(L, bf16, R, D, F, E, h, expert_off, w, nullptr, nullptr, y_perm));
+  if (moe::expert_gateup_save(L, R, D, F, E, x_perm, expert_off, w, a, gu, h) != cudaSuccess) return MOE_ERR_CUDA;
+  return cuda_status(moe::expert_down(L, true, R, D, F, E, h, expert_off, w, nullptr, nullptr, y_perm));
 }
 
 size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T) {

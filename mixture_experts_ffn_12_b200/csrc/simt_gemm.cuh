@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(256)
     simt_grouped_gemm_f32(const float* __restrict__ A, const float* __restrict__ B0, const float* __restrict__ B1,
                           const GemmArgs args) {
   pdl_enter();
-  constexpr bool kTwo = EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_SAVE;
+  constexpr bool kTwo = EPI == EPI_SWIGLU;
   __shared__ float sa[kSimtBK][kSimtBM + 4];
   __shared__ float sb0[kSimtBK][kSimtBN + 4];
   __shared__ float sb1[kTwo ? kSimtBK : 1][kTwo ? kSimtBN + 4 : 1];
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256)
     }
     __syncthreads();
   }
-  const float* bias0 = static_cast<const float*>(args.bias0) + static_cast<size_t>(g) * N;   // SAVE: may be absent
+  const float* bias0 = static_cast<const float*>(args.bias0) + static_cast<size_t>(g) * N;
   const float* bias1 = kTwo ? static_cast<const float*>(args.bias1) + static_cast<size_t>(g) * N : nullptr;
   float* out = static_cast<float*>(args.out);
 #pragma unroll
@@ -107,15 +107,6 @@ __global__ void __launch_bounds__(256)
         const float gc = fminf(fmaxf(acc0[i][j] + bias0[n], args.gate_lo), args.limit);
         const float uc = fminf(fmaxf(acc1[i][j] + bias1[n], -args.limit), args.limit);
         v = gc * uc / (1.0f + expf(-args.alpha * gc));
-      } else if constexpr (EPI == EPI_SWIGLU_SAVE) {
-        const float gv = args.bias0 == nullptr ? acc0[i][j] : acc0[i][j] + bias0[n];
-        const float uv = args.bias1 == nullptr ? acc1[i][j] : acc1[i][j] + bias1[n];
-        const float gc = fminf(fmaxf(gv, args.gate_lo), args.limit);
-        const float uc = fminf(fmaxf(uv, -args.limit), args.limit);
-        v = gc / (1.0f + expf(-args.alpha * gc)) * uc;
-        float* gu = static_cast<float*>(args.gu) + orow * 2 * N;
-        gu[n] = gv;
-        gu[N + n] = uv;
       } else if constexpr (EPI == EPI_BIAS_WSCATTER) {
         v = wv * (acc0[i][j] + bias0[n]);
       } else {

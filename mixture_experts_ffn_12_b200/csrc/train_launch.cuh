@@ -5,6 +5,7 @@
 #include "ffn_backward.cuh"
 #include "gemm_launch.cuh"
 #include "grouped_gemm_mx4.cuh"
+#include "simt_train.cuh"
 
 namespace moe {
 
@@ -113,7 +114,7 @@ cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const u
 // ---------------------------------------------------------------------------
 // expert block, training pass
 // ---------------------------------------------------------------------------
-cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
+cudaError_t expert_gateup_save(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
                                const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
                                void* h) {
   GemmArgs a = base_args(L);
@@ -130,14 +131,6 @@ cudaError_t expert_gateup_save(const Launch& L, bool bf16, int64_t R, int D, int
   a.out = h;
   a.ldo = F;
   a.gu = gu;
-  if (!bf16) {
-    const dim3 grid((F + kSimtBN - 1) / kSimtBN, static_cast<unsigned>((R + kSimtBM - 1) / kSimtBM + E));
-    pdl_launch(simt_grouped_gemm_f32<EPI_SWIGLU_SAVE>, dim3(grid), dim3(256), 0, L.stream,
-               static_cast<const float*>(x_perm), static_cast<const float*>(w.w_gate),
-               static_cast<const float*>(w.w_up), a);
-    count_launch();
-    return cudaGetLastError();
-  }
   CUtensorMap ta, tg, tu;
   cudaError_t e;
   if ((e = make_tmap(&ta, x_perm, false, D, R, 0, kBM)) != cudaSuccess) return e;
@@ -228,57 +221,76 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   return grad_f32 ? launch_backward<BWD_DW, float>(L, a, tiles) : launch_backward<BWD_DW, __nv_bfloat16>(L, a, tiles);
 }
 
-static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
+// ---------------------------------------------------------------------------
+// fp32 layers
+// ---------------------------------------------------------------------------
+static SimtTrainArgs simt_args(int64_t R, int E, const int32_t* off, const Activation& act) {
+  SimtTrainArgs a{};
+  a.group_off = off;
+  a.num_groups = E;
+  a.m_total = static_cast<int>(R);
+  a.limit = act.limit;
+  a.alpha = act.alpha;
+  a.gate_lo = act.gate_lo;
+  return a;
+}
+
+static unsigned simt_blocks(int64_t n, int tile) { return static_cast<unsigned>((n + tile - 1) / tile); }
+
+template <int KIND>
+static cudaError_t launch_simt(const Launch& L, const SimtTrainArgs& args, dim3 grid) {
+  constexpr int smem = SimtShape<KIND>::kSmem;
+  const cudaError_t e = allow_smem<simt_train_kernel<KIND>>(smem);
+  if (e != cudaSuccess) return e;
+  pdl_launch(simt_train_kernel<KIND>, grid, dim3(kStThreads), smem, L.stream, args);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t expert_train_f32(const Launch& L, int64_t R, int D, int F, int E, const float* x_perm,
+                             const int32_t* off, const ExpertWeights& w, const Activation& act, float* gu, float* h,
+                             float* y_perm) {
+  const unsigned row_tiles = simt_blocks(R, kStM) + E;
+  SimtTrainArgs a = simt_args(R, E, off, act);
+  auto f = [](const void* p) { return static_cast<const float*>(p); };
+  a.gu_out = gu;
+  a.job[0] = SimtJob{x_perm, f(w.w_gate), f(w.w_up), f(w.b_gate), f(w.b_up), h, nullptr, D, D, 0, F, D};
+  const cudaError_t e = launch_simt<SIMT_GATEUP>(L, a, dim3(row_tiles, simt_blocks(F, SimtShape<SIMT_GATEUP>::kStN)));
+  if (e != cudaSuccess) return e;
+  a.job[0] = SimtJob{h, f(w.w_down), nullptr, f(w.b_down), nullptr, y_perm, nullptr, F, F, 0, D, F};
+  return launch_simt<SIMT_DOWN>(L, a, dim3(row_tiles, simt_blocks(D, SimtShape<SIMT_DOWN>::kStN)));
+}
+
+static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F, int E, const float* x_perm,
                                        const int32_t* off, const ExpertWeights& w, const Activation& act,
-                                       const void* gu, const void* h, const void* dy, void* dgu, void* dx,
+                                       const float* gu, const float* h, const float* dy, float* dgu, float* dx,
                                        const ExpertGrads& gr) {
-  SimtBwdArgs p{};
-  p.group_off = off;
-  p.num_groups = E;
-  p.m_total = static_cast<int>(R);
-  p.limit = act.limit;
-  p.alpha = act.alpha;
-  p.gate_lo = act.gate_lo;
-  const unsigned row_tiles = static_cast<unsigned>((R + kSimtBM - 1) / kSimtBM + E);
-  auto col_tiles = [](int n) { return static_cast<unsigned>((n + kSimtBN - 1) / kSimtBN); };
+  const unsigned row_tiles = simt_blocks(R, kStM) + E;
+  SimtTrainArgs a = simt_args(R, E, off, act);
+  auto f = [](const void* p) { return static_cast<const float*>(p); };
+  cudaError_t e;
   if (dx != nullptr || gr.w_gate != nullptr || gr.w_up != nullptr) {
-    p.n = F;
-    p.k = D;
-    p.a = static_cast<const float*>(dy);
-    p.b0 = static_cast<const float*>(w.w_down);
-    p.gu = static_cast<const float*>(gu);
-    p.out = static_cast<float*>(dgu);
-    pdl_launch(simt_backward_kernel<BWD_DH>, dim3(col_tiles(F), row_tiles), dim3(256), 0, L.stream, p);
-    count_launch();
+    a.gu = gu;
+    a.job[0] = SimtJob{dy, f(w.w_down), nullptr, nullptr, nullptr, dgu, nullptr, D, F, 0, F, D};
+    if ((e = launch_simt<SIMT_DH>(L, a, dim3(row_tiles, simt_blocks(F, SimtShape<SIMT_DH>::kStN)))) != cudaSuccess) return e;
   }
   if (dx != nullptr) {
-    p.n = D;
-    p.k = F;
-    p.a = static_cast<const float*>(dgu);
-    p.b0 = static_cast<const float*>(w.w_gate);
-    p.b1 = static_cast<const float*>(w.w_up);
-    p.out = static_cast<float*>(dx);
-    pdl_launch(simt_backward_kernel<BWD_DX>, dim3(col_tiles(D), row_tiles), dim3(256), 0, L.stream, p);
-    count_launch();
+    a.job[0] = SimtJob{dgu, f(w.w_gate), f(w.w_up), nullptr, nullptr, dx, nullptr, 2 * F, D, 0, D, F};
+    if ((e = launch_simt<SIMT_DX>(L, a, dim3(row_tiles, simt_blocks(D, SimtShape<SIMT_DX>::kStN)))) != cudaSuccess) return e;
   }
-  auto grad = [&](void* out, void* bias_out, const void* pa, int m, int lda, const void* pb, int n) {
+  int jobs = 0, most_m = 0, most_n = 0;
+  auto add = [&](void* out, void* bias_out, const float* pa, int m, int lda, const float* pb, int n) {
     if (out == nullptr) return;
-    p.out = static_cast<float*>(out);
-    p.bias_out = static_cast<float*>(bias_out);
-    p.a = static_cast<const float*>(pa);
-    p.b0 = static_cast<const float*>(pb);
-    p.m = m;
-    p.n = n;
-    p.lda = lda;
-    p.ldb = n;
-    pdl_launch(simt_backward_kernel<BWD_DW>, dim3(col_tiles(n), static_cast<unsigned>((m + kSimtBM - 1) / kSimtBM), E),
-               dim3(256), 0, L.stream, p);
-    count_launch();
+    a.job[jobs++] = SimtJob{pa, pb, nullptr, nullptr, nullptr, static_cast<float*>(out), static_cast<float*>(bias_out),
+                            lda, n, m, n, 0};
+    most_m = std::max(most_m, m);
+    most_n = std::max(most_n, n);
   };
-  grad(gr.w_down, gr.b_down, dy, D, D, h, F);
-  grad(gr.w_gate, gr.b_gate, dgu, F, 2 * F, x_perm, D);
-  grad(gr.w_up, gr.b_up, static_cast<float*>(dgu) + F, F, 2 * F, x_perm, D);
-  return cudaGetLastError();
+  add(gr.w_down, gr.b_down, dy, D, D, h, F);
+  add(gr.w_gate, gr.b_gate, dgu, F, 2 * F, x_perm, D);
+  add(gr.w_up, gr.b_up, dgu + F, F, 2 * F, x_perm, D);
+  if (jobs == 0) return cudaSuccess;
+  return launch_simt<SIMT_DW>(L, a, dim3(simt_blocks(most_m, kStM), simt_blocks(most_n, SimtShape<SIMT_DW>::kStN), jobs * E));
 }
 
 cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
@@ -287,7 +299,9 @@ cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F,
                             bool grad_f32) {
   if (bf16)
     return expert_backward_bf16(L, R, D, F, E, x_perm, expert_off, w, act, gu, h, dy, dgu, dx, grads, grad_f32);
-  return expert_backward_f32(L, R, D, F, E, x_perm, expert_off, w, act, gu, h, dy, dgu, dx, grads);
+  return expert_backward_f32(L, R, D, F, E, static_cast<const float*>(x_perm), expert_off, w, act,
+                             static_cast<const float*>(gu), static_cast<const float*>(h),
+                             static_cast<const float*>(dy), static_cast<float*>(dgu), static_cast<float*>(dx), grads);
 }
 
 cudaError_t combine_backward(const Launch& L, bool bf16, int64_t T, int D, int k, const void* dy, const void* y_perm,
