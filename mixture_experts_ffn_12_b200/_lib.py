@@ -116,6 +116,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """The loaded library (built in-tree by mixture_experts_ffn_12_b200.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -79,6 +79,9 @@ def _p(t: Optional[torch.Tensor]):
 # --------------------------------------------------------------------------- #
 def _want(name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype,
           device: Optional[torch.device] = None) -> None:
+    if (t is not None and t.shape == shape and t.dtype is dtype and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if tuple(t.shape) != tuple(shape):
@@ -183,6 +186,22 @@ def check_layer_args(cfg: MoeConfig, x, w_router, b_router, weights: Optional["E
 
 def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _launch(what: str, device: torch.device, *args) -> None:
+    """Calls the library function `what` with torch's current stream of `device` behind args, that device
+    current.  Tensors in args are checked ones (``_want``): their addresses are passed."""
+    if device.type != "cuda":
+        raise ValueError("libmoe takes CUDA tensors")
+    fn = getattr(_lib.load(), what)
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if code != _lib.MOE_OK:
+        raise MoeError(code, what)
 
 
 @dataclasses.dataclass
@@ -464,15 +483,15 @@ def quantize_mxfp4(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     layout of MXFP4 expert weights (moe_quantize_mxfp4)."""
     if x.dim() < 1 or x.dtype not in _DT_OF:
         raise ValueError("quantize_mxfp4 takes a bf16 or fp32 tensor of at least one dimension")
+    if not x.is_contiguous():
+        raise ValueError("quantize_mxfp4: x must be contiguous")
     K = x.shape[-1]
     if K == 0 or K % 32:
         raise ValueError(f"quantize_mxfp4: the last dimension ({K}) must be a positive multiple of 32")
     lead = x.shape[:-1]
     codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
     scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(_lib.load().moe_quantize_mxfp4(x.numel() // K, K, _DT_OF[x.dtype], _p(x), _p(codes), _p(scales),
-                                              _stream(x.device)), "moe_quantize_mxfp4")
+    _launch("moe_quantize_mxfp4", x.device, x.numel() // K, K, _DT_OF[x.dtype], x, codes, scales)
     return codes, scales
 
 
@@ -480,6 +499,8 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
     """The values of quantize_mxfp4's codes and scales, [..., K] in dtype (exact; NaN for scale byte 255)."""
     if codes.dim() < 1 or codes.dtype != torch.uint8:
         raise ValueError("dequantize_mxfp4 takes uint8 codes [..., K/2]")
+    if not codes.is_contiguous():
+        raise ValueError("dequantize_mxfp4: codes must be contiguous")
     if dtype not in _DT_OF:
         raise ValueError("dequantize_mxfp4 gives bf16 or fp32")
     K = 2 * codes.shape[-1]
@@ -487,9 +508,7 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
         raise ValueError(f"dequantize_mxfp4: K = {K} must be a positive multiple of 32")
     _want("scales", scales, (*codes.shape[:-1], K // 32), torch.uint8, codes.device)
     out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
-    with torch.cuda.device(codes.device):
-        _check(_lib.load().moe_dequantize_mxfp4(out.numel() // K, K, _p(codes), _p(scales), _DT_OF[dtype], _p(out),
-                                                _stream(codes.device)), "moe_dequantize_mxfp4")
+    _launch("moe_dequantize_mxfp4", codes.device, out.numel() // K, K, codes, scales, _DT_OF[dtype], out)
     return out
 
 
@@ -511,12 +530,11 @@ def mxfp4_weights(codes: torch.Tensor, scales: torch.Tensor) -> Mxfp4Weights:
     """codes [G, N, K/2], scales [G, N, K/32] (quantize_mxfp4's, or MXFP4 expert weights) -> Mxfp4Weights."""
     G, N, K = _mxfp4_sizes(codes)
     L = _lib.load()
+    _want("codes", codes, (G, N, K // 2), torch.uint8)
     _want("scales", scales, (G, N, K // 32), torch.uint8, codes.device)
     n = _size(L.moe_mxfp4_weight_tiles_size(G, N, K), "moe_mxfp4_weight_tiles_size")
     tiles = torch.empty(n, dtype=torch.uint8, device=codes.device)
-    with torch.cuda.device(codes.device):
-        _check(L.moe_mxfp4_weight_tiles(G, N, K, _p(scales), _p(tiles), _stream(codes.device)),
-               "moe_mxfp4_weight_tiles")
+    _launch("moe_mxfp4_weight_tiles", codes.device, G, N, K, scales, tiles)
     return Mxfp4Weights(codes, tiles)
 
 
@@ -557,10 +575,8 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] 
         ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
     elif ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, expected {dev}")
-    with torch.cuda.device(dev):
-        _check(L.moe_mxfp4_linear(G, R, N, K, _p(x), _p(group_off), _p(w.codes), _p(w.tiles), _p(bias),
-                                  1 if out_f32 else 0, _p(y), _p(ws), ws.numel() * ws.element_size(), _stream(dev)),
-               "moe_mxfp4_linear")
+    _launch("moe_mxfp4_linear", dev, G, R, N, K, x, group_off, w.codes, w.tiles, bias, 1 if out_f32 else 0, y, ws,
+            ws.numel() * ws.element_size())
     return y
 
 
@@ -632,9 +648,8 @@ def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Ten
         nws = _size(L.moe_expert_ffn_train_workspace_size(ctypes.byref(cfg), T), "moe_expert_ffn_train_workspace_size")
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
     wst = weights.c_struct()
-    with torch.cuda.device(dev):
-        _check(L.moe_expert_ffn_train(ctypes.byref(cfg), code, T, _p(x_perm), _p(expert_off), ctypes.byref(wst),
-                                      _p(gu), _p(h), _p(y), _p(ws), nws, _stream(dev)), "moe_expert_ffn_train")
+    _launch("moe_expert_ffn_train", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h, y,
+            ws, nws)
     return gu, h, y
 
 
@@ -689,10 +704,8 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
     elif ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, expected {dev}")
     wst, gst = weights.c_struct(), grads.c_struct()
-    with torch.cuda.device(dev):
-        _check(L.moe_expert_ffn_backward(ctypes.byref(cfg), code, T, _p(x_perm), _p(expert_off), ctypes.byref(wst),
-                                         _p(gu), _p(h), _p(dy_perm), _p(dx), ctypes.byref(gst), _p(ws),
-                                         ws.numel() * ws.element_size(), _stream(dev)), "moe_expert_ffn_backward")
+    _launch("moe_expert_ffn_backward", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h,
+            dy_perm, dx, ctypes.byref(gst), ws, ws.numel() * ws.element_size())
     return dx, grads
 
 
@@ -704,9 +717,7 @@ def combine_backward(cfg: MoeConfig, dy: torch.Tensor, y_perm: torch.Tensor, row
     _want("dy", dy, (T, cfg.hidden_size), torch_dtype(cfg), dev)
     dy_perm = torch.empty_like(y_perm)
     dw = torch.empty_like(topk_w)
-    with torch.cuda.device(dev):
-        _check(_lib.load().moe_combine_backward(ctypes.byref(cfg), T, _p(dy), _p(y_perm), _p(row_of_slot), _p(topk_w),
-                                                _p(dy_perm), _p(dw), _stream(dev)), "moe_combine_backward")
+    _launch("moe_combine_backward", dev, ctypes.byref(cfg), T, dy, y_perm, row_of_slot, topk_w, dy_perm, dw)
     return dy_perm, dw
 
 
