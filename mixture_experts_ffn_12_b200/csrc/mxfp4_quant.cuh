@@ -8,9 +8,10 @@
 // and a block that holds an infinity or a NaN gets scale byte 255 (the E8M0 NaN) and
 // zero codes, so that it reads back as NaN instead of as a wrong number.
 //
-// Bound by memory: 2 (bf16) or 4 (fp32) bytes read and 0.53 written an element.  Four
-// lanes share a block (8 elements each, one or two 16-byte loads): every load and store
-// of a warp is contiguous, and the block maximum takes two shuffles.
+// Bound by memory: 2 (bf16) or 4 (fp32) bytes read and 0.53 written an element.  Four lanes
+// share a block (8 elements each): every 16-byte load and 4-byte store of a warp is one run
+// (two lanes a block, 32 bytes a lane, were slower), the block maximum takes two shuffles;
+// bf16 maxima and scaling run on packed pairs.
 //
 // Scale layouts.  "Rows": [rows, K/32], what the MXFP4 expert weights of the layer use.
 // "Tiles": what the 4-bit x 4-bit product reads: for 128 rows and 128 elements of K one
@@ -45,64 +46,135 @@ __device__ __forceinline__ int mx4_exponent(uint32_t amax_bits) {
   return max(-127, (ef - 127) - 2 + ((amax_bits & 0x7FFFFFu) > 0x400000u ? 1 : 0));
 }
 
-// Two floats to E2M1, round to nearest even, `lo` in the low nibble.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight floats to E2M1 codes, round to nearest even, v[0] in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 
-// Two E2M1 codes (low nibble first) to two floats.
-__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t byte) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.u8.u32 t, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-      : "=r"(h)
-      : "r"(byte));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// Eight E2M1 codes (low nibble first) to floats.
+__device__ __forceinline__ void e2m1x8_to_f32(uint32_t q, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
 }
 
-// 8 elements of a block that four neighbouring lanes share -> 8 codes and the scale byte.
-__device__ __forceinline__ uint32_t mx4_quantize8(const float (&v)[8], uint32_t& scale) {
-  uint32_t m = 0;
+// 8 elements as loaded, to floats.
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4* raw, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __bfloat1622float2(h[j]);
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
+  } else {
+    const float* f = reinterpret_cast<const float*>(raw);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+  }
+}
+
+// 8 elements of a block that four neighbouring lanes share, as loaded: 8 codes and the scale
+// byte.
+template <typename T>
+__device__ __forceinline__ uint32_t mx4_quantize8(const uint4* raw, uint32_t& scale) {
+  uint32_t m;
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(raw);   // |x| orders as its bits do
+    uint32_t m2 = __vmaxu2(__vmaxu2(r[0] & 0x7FFF7FFFu, r[1] & 0x7FFF7FFFu),
+                           __vmaxu2(r[2] & 0x7FFF7FFFu, r[3] & 0x7FFF7FFFu));
+    m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+    m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
+    m = max(m2 & 0xFFFFu, m2 >> 16) << 16;
+  } else {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(raw);
+    m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, r[j] & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  }
   if (m >= 0x7F800000u) {   // an infinity or a NaN in the block
     scale = 255;
     return 0;
   }
   const int X = mx4_exponent(m);
   scale = static_cast<uint32_t>(X + 127);
-  const float inv = exp2_int(-X);
-  uint32_t q = 0;
+  float v[8];
+  if constexpr (sizeof(T) == 2) {
+    const uint16_t ib = static_cast<uint16_t>((127 - X) << 7);    // 2^-X, X in [-127, 126]
+    const __nv_bfloat162 inv = __halves2bfloat162(__ushort_as_bfloat16(ib), __ushort_as_bfloat16(ib));
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
-  return q;
+    for (int j = 0; j < 4; ++j) {   // exact, or so small that it rounds to zero either way
+      const float2 f = __bfloat1622float2(__hmul2(h[j], inv));
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
+  } else {
+    const float inv = exp2_int(-X);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = reinterpret_cast<const float*>(raw)[j] * inv;
+  }
+  return e2m1x8(v);
 }
 
 // x [nblk, 32] -> codes [nblk, 16 B], scales [nblk]: rows of any width are runs of blocks.
+// A thread loads kMx4Unroll pieces before it uses the first (one load at a time leaves 32 KB
+// a SM outstanding, too little for HBM).
+constexpr int kMx4Unroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const T* __restrict__ x, int64_t nblk,
                                                              uint32_t* __restrict__ codes,
                                                              uint8_t* __restrict__ scales) {
   pdl_enter();
   const int64_t total = nblk * 4;   // lanes; whole warps take part in the shuffles
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < total; i += step) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (i < total) load8<T>(x + i * 8, v);
-    uint32_t s;
-    const uint32_t q = mx4_quantize8(v, s);
-    if (i < total) {
-      codes[i] = q;
-      if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(s);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * kMx4Unroll;
+  constexpr int kWords = sizeof(T) / 2;   // 16-byte words of 8 elements
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * 256 * kMx4Unroll; base < total; base += step) {
+    const uint4* src = reinterpret_cast<const uint4*>(x) + base * kWords;
+    uint32_t* dst = codes + base;
+    uint8_t* sdst = scales + (base >> 2);
+    const int left = static_cast<int>(min(total - base, static_cast<int64_t>(256 * kMx4Unroll)));
+    uint4 raw[kMx4Unroll][kWords];
+#pragma unroll
+    for (int u = 0; u < kMx4Unroll; ++u) {
+      const int i = u * 256 + threadIdx.x;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) raw[u][w] = i < left ? __ldcs(src + i * kWords + w) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kMx4Unroll; ++u) {
+      const int i = u * 256 + threadIdx.x;
+      uint32_t s;
+      const uint32_t q = mx4_quantize8<T>(raw[u], s);
+      if (i < left) {
+        dst[i] = q;
+        if ((i & 3) == 0) sdst[i >> 2] = static_cast<uint8_t>(s);
+      }
     }
   }
 }
@@ -143,13 +215,13 @@ __device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int r
 
 // x [rows, K] bf16, rows grouped by off (null: one group) -> codes [rows, K/2] and scale
 // tiles, the row tiles counted group after group.  Rows outside every group are skipped.
-// A warp takes up to kMx4QuantSpan elements of a row (all loads in flight before the first
-// is used); the row's place in the tiles is looked up once, and the scales of 128 elements
-// (four blocks, 16 lanes) leave as one 4-byte word.
+// A warp takes `spans` runs of kMx4QuantSpan elements of a row (blockIdx.y picks which): the
+// row's place in the tiles is looked up once, all loads of a run are in flight before the
+// first is used, and the scales of 128 elements (four blocks, 16 lanes) leave as one word.
 constexpr int kMx4QuantSpan = 1024;
 __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, int rows, int K,
                                                               const int32_t* __restrict__ off, int G, int max_tiles,
-                                                              uint32_t* __restrict__ codes,
+                                                              int spans, uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ tiles) {
   pdl_enter();
   __shared__ int goff[kMaxGroups + 2];
@@ -158,55 +230,52 @@ __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat1
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const int kc = mx4_chunks(K);
-  const int spans = (K + kMx4QuantSpan - 1) / kMx4QuantSpan;
-  const int64_t total = static_cast<int64_t>(rows) * spans;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const int k_first = blockIdx.y * spans * kMx4QuantSpan;
+  const int k_end = min(k_first + spans * kMx4QuantSpan, kc * 128);
+  const int step = gridDim.x * 8;
   constexpr int IT = kMx4QuantSpan / 256;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < total; i += step) {
-    const int row = static_cast<int>(i / spans);
-    const int k0 = static_cast<int>(i - static_cast<int64_t>(row) * spans) * kMx4QuantSpan + lane * 8;
+  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += step) {
     const __nv_bfloat16* src = x + static_cast<size_t>(row) * K;
-    uint4 raw[IT];
+    uint32_t* crow = codes + (static_cast<size_t>(row) * K >> 3);
+    uint8_t* dst = nullptr;
+    for (int kb = k_first; kb < k_end; kb += kMx4QuantSpan) {
+      uint4 raw[IT];
 #pragma unroll
-    for (int t = 0; t < IT; ++t)
-      raw[t] = k0 + 256 * t < K ? *reinterpret_cast<const uint4*>(src + k0 + 256 * t) : make_uint4(0, 0, 0, 0);
-    int lo = 0, hi = G;   // goff[lo] <= row < goff[hi] where the row is in a group
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (goff[mid] <= row) lo = mid; else hi = mid;
-    }
-    const int grows = goff[lo + 1] - goff[lo], rt = tile_off[lo + 1] - tile_off[lo];
-    int p = row - goff[lo], tile = 0;
-    bool in = p >= 0 && p < grows;
-    if (in) {
-      const int per = mx4_rows_per_tile(grows, rt);
-      tile = p / per;
-      p -= tile * per;
-      tile += tile_off[lo];
-      in = tile < max_tiles;   // offsets that are not ascending (flagged)
-    }
-    uint8_t* dst = tiles + static_cast<size_t>(tile) * kc * 1024 + 512 * (p >> 7) + 16 * (p & 31) + 4 * ((p & 127) >> 5);
-#pragma unroll
-    for (int t = 0; t < IT; ++t) {
-      const int k = k0 + 256 * t;
-      float v[8];
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw[t]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __bfloat1622float2(h[j]);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
+      for (int t = 0; t < IT; ++t) {
+        const int k = kb + 256 * t + lane * 8;
+        raw[t] = k < K ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0, 0, 0, 0);
       }
-      uint32_t s;
-      const uint32_t q = mx4_quantize8(v, s);
-      if (k < K) codes[(static_cast<size_t>(row) * K + k) >> 3] = q;
-      // lanes 0, 4, 8, 12 of each half warp hold the scales of a chunk's four blocks
-      if (k >= K) s = 127;
-      uint32_t w = s << (8 * ((lane >> 2) & 3));
-      w |= __shfl_xor_sync(0xffffffffu, w, 4);
-      w |= __shfl_xor_sync(0xffffffffu, w, 8);
-      const int c = k >> 7;
-      if (in && (lane & 15) == 0 && c < kc) *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(c) * 1024) = w;
+      if (kb == k_first) {
+        int lo = 0, hi = G;   // goff[lo] <= row < goff[hi] where the row is in a group
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (goff[mid] <= row) lo = mid; else hi = mid;
+        }
+        const int grows = goff[lo + 1] - goff[lo];
+        int p = row - goff[lo];
+        if (p >= 0 && p < grows) {
+          const int per = mx4_rows_per_tile(grows, tile_off[lo + 1] - tile_off[lo]);
+          const int t = p / per;
+          p -= t * per;
+          const int tile = tile_off[lo] + t;
+          if (tile < max_tiles)   // else: offsets that are not ascending (flagged)
+            dst = tiles + static_cast<size_t>(tile) * kc * 1024 + 512 * (p >> 7) + 16 * (p & 31) + 4 * ((p & 127) >> 5);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+        const int k = kb + 256 * t + lane * 8;
+        uint32_t s;
+        const uint32_t q = mx4_quantize8<__nv_bfloat16>(&raw[t], s);
+        if (k < K) crow[k >> 3] = q;
+        else s = 127;
+        // lanes 0, 4, 8, 12 of each half warp hold the scales of a chunk's four blocks
+        uint32_t w = s << (8 * ((lane >> 2) & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        w |= __shfl_xor_sync(0xffffffffu, w, 8);
+        if (dst != nullptr && (lane & 15) == 0 && k < kc * 128)
+          *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(k >> 7) * 1024) = w;
+      }
     }
   }
 }
@@ -245,19 +314,30 @@ __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* _
                                                                T* __restrict__ out) {
   pdl_enter();
   const int64_t total = nblk * 4;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-    const uint32_t q = codes[i];
-    const int s = scales[i >> 2];
-    const float f = s == 255 ? __uint_as_float(0x7FC00000u) : exp2_int(s - 127);
-    float v[8];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * kMx4Unroll;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * 256 * kMx4Unroll; base < total; base += step) {
+    const uint32_t* src = codes + base;
+    const uint8_t* ssrc = scales + (base >> 2);
+    T* dst = out + base * 8;
+    const int left = static_cast<int>(min(total - base, static_cast<int64_t>(256 * kMx4Unroll)));
+    uint32_t q[kMx4Unroll];
+    int s[kMx4Unroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = e2m1x2_to_f32((q >> (8 * j)) & 0xFFu);
-      v[2 * j] = p.x * f;
-      v[2 * j + 1] = p.y * f;
+    for (int u = 0; u < kMx4Unroll; ++u) {
+      const int i = u * 256 + threadIdx.x;
+      q[u] = i < left ? src[i] : 0;
+      s[u] = i < left ? ssrc[i >> 2] : 0;
     }
-    store8<T>(out + i * 8, v);
+#pragma unroll
+    for (int u = 0; u < kMx4Unroll; ++u) {
+      const int i = u * 256 + threadIdx.x;
+      const float f = s[u] == 255 ? __uint_as_float(0x7FC00000u) : exp2_int(s[u] - 127);
+      float v[8];
+      e2m1x8_to_f32(q[u], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= f;
+      if (i < left) store8<T>(dst + i * 8, v);
+    }
   }
 }
 
@@ -268,7 +348,7 @@ static int mx4_blocks(const Launch& L, int64_t threads) {
 cudaError_t mx4_quant_rows(const Launch& L, bool bf16, int64_t rows, int K, const void* x, uint8_t* codes,
                            uint8_t* scales) {
   const int64_t nblk = rows * (K / 32);
-  const int blocks = mx4_blocks(L, nblk * 4);
+  const int blocks = mx4_blocks(L, nblk * 4 / kMx4Unroll + 1);
   if (bf16)
     pdl_launch(mx4_quant_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, L.stream,
                static_cast<const __nv_bfloat16*>(x), nblk, reinterpret_cast<uint32_t*>(codes), scales);
@@ -282,7 +362,7 @@ cudaError_t mx4_quant_rows(const Launch& L, bool bf16, int64_t rows, int K, cons
 cudaError_t mx4_dequant_rows(const Launch& L, bool bf16, int64_t rows, int K, const uint8_t* codes,
                              const uint8_t* scales, void* out) {
   const int64_t nblk = rows * (K / 32);
-  const int blocks = mx4_blocks(L, nblk * 4);
+  const int blocks = mx4_blocks(L, nblk * 4 / kMx4Unroll + 1);
   if (bf16)
     pdl_launch(mx4_dequant_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, L.stream,
                reinterpret_cast<const uint32_t*>(codes), scales, nblk, static_cast<__nv_bfloat16*>(out));
@@ -309,10 +389,13 @@ size_t mx4_row_tiles_bytes(int64_t R, int G, int K) {
 
 cudaError_t mx4_quant_tiles(const Launch& L, int64_t R, int K, const void* x, const int32_t* off, int G,
                             uint8_t* codes, uint8_t* tiles) {
-  const int64_t warps = R * ((K + kMx4QuantSpan - 1) / kMx4QuantSpan);
-  pdl_launch(mx4_quant_tiles_kernel, dim3(mx4_blocks(L, warps * 32)), dim3(256), 0, L.stream,
+  // many rows: a warp takes whole rows; few: every run of a row is a warp of its own
+  const int runs = (K + kMx4QuantSpan - 1) / kMx4QuantSpan;
+  const int spans = R >= int64_t(32) * L.num_sms ? runs : 1;
+  const unsigned bx = static_cast<unsigned>(std::min<int64_t>((R + 7) / 8, int64_t(L.num_sms) * 8));
+  pdl_launch(mx4_quant_tiles_kernel, dim3(bx, (runs + spans - 1) / spans), dim3(256), 0, L.stream,
              static_cast<const __nv_bfloat16*>(x), static_cast<int>(R), K, off, G,
-             static_cast<int>(mx4_row_tiles(R, G)), reinterpret_cast<uint32_t*>(codes), tiles);
+             static_cast<int>(mx4_row_tiles(R, G)), spans, reinterpret_cast<uint32_t*>(codes), tiles);
   count_launch();
   return cudaGetLastError();
 }

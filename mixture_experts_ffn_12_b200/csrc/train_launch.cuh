@@ -304,18 +304,22 @@ cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F,
                              static_cast<const float*>(dy), static_cast<float*>(dgu), static_cast<float*>(dx), grads);
 }
 
+template <typename T, int KM>
+static void launch_combine_backward(const Launch& L, int64_t Tn, int D, int k, const void* dy, const void* y_perm,
+                                    const int32_t* row_of_slot, const float* w, void* dy_perm, float* dw) {
+  const int threads = std::min(kCombineBwdThreads, (D / 8 + 31) / 32 * 32);
+  pdl_launch(combine_backward_kernel<T, KM>, dim3(static_cast<unsigned>(Tn)), dim3(threads), 0, L.stream,
+             static_cast<const T*>(dy), static_cast<const T*>(y_perm), row_of_slot, w, static_cast<int>(Tn), k, D,
+             static_cast<T*>(dy_perm), dw);
+  count_launch();
+}
+
 cudaError_t combine_backward(const Launch& L, bool bf16, int64_t T, int D, int k, const void* dy, const void* y_perm,
                              const int32_t* row_of_slot, const float* w, void* dy_perm, float* dw) {
-  const dim3 grid(static_cast<unsigned>(T)), block(kCombineBwdThreads);
-  if (bf16)
-    pdl_launch(combine_backward_kernel<__nv_bfloat16>, grid, block, 0, L.stream,
-               static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(y_perm), row_of_slot, w,
-               static_cast<int>(T), k, D, static_cast<__nv_bfloat16*>(dy_perm), dw);
-  else
-    pdl_launch(combine_backward_kernel<float>, grid, block, 0, L.stream, static_cast<const float*>(dy),
-               static_cast<const float*>(y_perm), row_of_slot, w, static_cast<int>(T), k, D,
-               static_cast<float*>(dy_perm), dw);
-  count_launch();
+  if (bf16 && k <= 4) launch_combine_backward<__nv_bfloat16, 4>(L, T, D, k, dy, y_perm, row_of_slot, w, dy_perm, dw);
+  else if (bf16) launch_combine_backward<__nv_bfloat16, 8>(L, T, D, k, dy, y_perm, row_of_slot, w, dy_perm, dw);
+  else if (k <= 4) launch_combine_backward<float, 4>(L, T, D, k, dy, y_perm, row_of_slot, w, dy_perm, dw);
+  else launch_combine_backward<float, 8>(L, T, D, k, dy, y_perm, row_of_slot, w, dy_perm, dw);
   return cudaGetLastError();
 }
 

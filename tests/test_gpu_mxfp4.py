@@ -31,7 +31,9 @@ def _rows(rows, K, dtype, seed):
     a[1, :32] = np.resize([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, -0.25, -6.0], 32) * 2.0 ** -9   # ties
     a[2, :32] = 2.0 ** -130                                    # below the smallest scale's range
     a[3, :32] = np.ldexp(1.0, np.arange(-16, 16))              # one block over many binades
+    a[0, 40 % K], a[1, 50 % K] = 2.0 ** -127, -(2.0 ** -126)   # subnormal values at the smallest scale, and next to it
     if K >= 96:
+        a[0, 32:64] = 2.0 ** -127 * np.resize([1, 2, 3, 0.5, -1, 0.25], 32)   # a block of them
         a[2, 32:64] = 2.5e38                                   # largest magnitudes
         a[3, 40], a[3, 70] = np.inf, np.nan
     return torch.from_numpy(a[:rows].astype(np.float32)).cuda().to(dtype)
