@@ -418,12 +418,12 @@ typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_SILU = 1 } moe_act_t;
  *      so that the backward pass sees on which side of the clip it was,
  *      h [R, F] in dtype, y_perm [R, D] in dtype.
  * Dense weights in dtype; each of the biases may be NULL (none).  h_split and
- * MXFP4 weights: MOE_ERR_UNSUPPORTED.  With E = k = 1 it is a dense block.
- * ws: moe_expert_ffn_train_workspace_size bytes (may be NULL if b_down is not). */
-MOE_API size_t moe_expert_ffn_train_workspace_size(const moe_config_t* cfg, int64_t T);
+ * MXFP4 weights: MOE_ERR_UNSUPPORTED.  With E = k = 1 it is a dense block.  Rows
+ * that belong to no expert (behind expert_off[E]) are left as they are.  Not
+ * touched by moe_set_expert_gemm_variant. */
 MOE_API moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
                                           const int32_t* expert_off, const moe_expert_weights_t* weights, void* gu,
-                                          void* h, void* y_perm, void* ws, size_t ws_bytes, void* stream);
+                                          void* h, void* y_perm, void* stream);
 
 /* Gradients of the expert parameters, same layouts as the parameters, in dtype
  * or in fp32 (grad_f32 = 1).  A NULL pointer: not wanted; a bias gradient comes

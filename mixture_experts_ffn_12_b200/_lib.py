@@ -102,8 +102,7 @@ SIGNATURES = {
     "moe_mxfp4_weight_tiles": (_ST, [_I32, _I32, _I32, _P, _P, _P]),
     "moe_mxfp4_linear_workspace_size": (ctypes.c_size_t, [_I32, _I64, _I32, _I32]),
     "moe_mxfp4_linear": (_ST, [_I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P]),
-    "moe_expert_ffn_train_workspace_size": (ctypes.c_size_t, [_CFG, _I64]),
-    "moe_expert_ffn_train": (_ST, [_CFG, _I32, _I64, _P, _P, _W, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_expert_ffn_train": (_ST, [_CFG, _I32, _I64, _P, _P, _W, _P, _P, _P, _P]),
     "moe_expert_ffn_backward_workspace_size": (ctypes.c_size_t, [_CFG, _I64]),
     "moe_expert_ffn_backward": (_ST, [_CFG, _I32, _I64, _P, _P, _W, _P, _P, _P, _P, _GR, _P, ctypes.c_size_t, _P]),
     "moe_combine_backward": (_ST, [_CFG, _I64, _P, _P, _P, _P, _P, _P, _P]),

@@ -639,17 +639,12 @@ def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Ten
     act: "swiglu" (the layer's clipped SwiGLU) or "silu"; biases may be None."""
     code = _act_code(act)
     T = check_ffn_train_args(cfg, x_perm, expert_off, weights)
-    L, R, dev, dt = _lib.load(), x_perm.shape[0], x_perm.device, x_perm.dtype
+    R, dev, dt = x_perm.shape[0], x_perm.device, x_perm.dtype
     gu = torch.empty((R, 2, cfg.intermediate_size), dtype=dt, device=dev)
     h = torch.empty((R, cfg.intermediate_size), dtype=dt, device=dev)
     y = torch.empty((R, cfg.hidden_size), dtype=dt, device=dev)
-    ws, nws = None, 0
-    if weights.b_down is None:
-        nws = _size(L.moe_expert_ffn_train_workspace_size(ctypes.byref(cfg), T), "moe_expert_ffn_train_workspace_size")
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
     wst = weights.c_struct()
-    _launch("moe_expert_ffn_train", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h, y,
-            ws, nws)
+    _launch("moe_expert_ffn_train", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h, y)
     return gu, h, y
 
 

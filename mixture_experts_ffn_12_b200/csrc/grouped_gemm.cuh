@@ -16,9 +16,6 @@
 //                     done in the down projection's epilogue.
 //   EPI_TOPK          router: logits = C + b[n]; the k largest per row (ties -> lower
 //                     expert index) and the softmax over them.
-//   EPI_SWIGLU_SAVE   EPI_SWIGLU that also stores the pre-activations g and u (biases added,
-//                     before the clips) as rows [2, N], for the backward pass; the biases
-//                     may be absent.
 //   EPI_PARTIAL       router, K split: the tile's column block index selects one of
 //                     k_splits K ranges; the fp32 partial logits go to `partial`.
 //
@@ -48,14 +45,7 @@
 
 namespace moe {
 
-enum EpiKind : int {
-  EPI_SWIGLU = 0,
-  EPI_BIAS = 1,
-  EPI_BIAS_WSCATTER = 2,
-  EPI_TOPK = 3,
-  EPI_PARTIAL = 4,
-  EPI_SWIGLU_SAVE = 5
-};
+enum EpiKind : int { EPI_SWIGLU = 0, EPI_BIAS = 1, EPI_BIAS_WSCATTER = 2, EPI_TOPK = 3, EPI_PARTIAL = 4 };
 
 struct GemmArgs {
   const int32_t* group_off;    // [G+1] row offsets of the groups in A; nullptr = one group of m_total rows
@@ -87,7 +77,6 @@ struct GemmArgs {
                                // EPI_SWIGLU writes hi = bf16(h) and lo = bf16(h - hi); the down
                                // GEMM reads h through a 3-D tensor map {F, 2, R} and sums over
                                // both halves against the same weights (K = 2F).  0 or 1: one bf16 h.
-  void* gu;                    // EPI_SWIGLU_SAVE: [R, 2, n_out] pre-activations
 };
 
 constexpr int kBM = 128;           // rows per tile (MMA M)
@@ -173,52 +162,6 @@ __device__ __forceinline__ void epi_swiglu(uint32_t tbase, int row, bool rvalid,
           store8<T>(out + a.n_out + c, lo);
         }
       }
-    }
-  }
-}
-
-// v rounded to bf16, kept on its side of the bounds +-lim: the backward pass decides from the
-// stored value whether the clip let the gradient through, so rounding must not move it across.
-__device__ __forceinline__ float bf16_keep_side(float v, float lim) {
-  const float a = fabsf(v);
-  uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(a));
-  const bool over = a > lim;
-  if ((__bfloat162float(__ushort_as_bfloat16(b)) > lim) != over) b += over ? 1 : -1;
-  return copysignf(__bfloat162float(__ushort_as_bfloat16(b)), v);
-}
-
-template <typename T, int TN>
-__device__ __forceinline__ void epi_swiglu_save(uint32_t tbase, int row, bool rvalid, const TileInfo& ti,
-                                                const GemmArgs& a) {
-  const size_t goff = static_cast<size_t>(ti.g) * a.n_out + ti.n0;
-  const T* bg = a.bias0 == nullptr ? nullptr : static_cast<const T*>(a.bias0) + goff;
-  const T* bu = a.bias1 == nullptr ? nullptr : static_cast<const T*>(a.bias1) + goff;
-  T* out = static_cast<T*>(a.out) + static_cast<size_t>(row) * a.ldo + ti.n0;
-  T* gu = static_cast<T*>(a.gu) + static_cast<size_t>(row) * 2 * a.n_out + ti.n0;
-  const float L = a.limit, alpha = a.alpha;
-#pragma unroll 1
-  for (int c = 0; c < TN; c += 8) {
-    float g[8], u[8];
-    tmem_ld8(tbase + c, g);
-    tmem_ld8(tbase + TN + c, u);
-    tmem_ld_wait();
-    if (rvalid && ti.n0 + c < a.n_out) {
-      float b0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b1[8] = {0, 0, 0, 0, 0, 0, 0, 0}, h[8];
-      if (bg != nullptr) load8<T>(bg + c, b0);
-      if (bu != nullptr) load8<T>(bu + c, b1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        g[j] += b0[j];
-        u[j] += b1[j];
-        const float gc = fminf(fmaxf(g[j], a.gate_lo), L);
-        const float uc = fminf(fmaxf(u[j], -L), L);
-        h[j] = __fdividef(gc, 1.0f + __expf(-alpha * gc)) * uc;
-        g[j] = bf16_keep_side(g[j], L);
-        u[j] = bf16_keep_side(u[j], L);
-      }
-      store8<T>(out + c, h);
-      store8<T>(gu + c, g);
-      store8<T>(gu + a.n_out + c, u);
     }
   }
 }
@@ -586,7 +529,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int row = ti.m0 + r_in_tile;
       const bool rvalid = row < ti.m_end;
       if constexpr (EPI == EPI_SWIGLU) epi_swiglu<T, TN>(tbase, row, rvalid, ti, args);
-      else if constexpr (EPI == EPI_SWIGLU_SAVE) epi_swiglu_save<T, TN>(tbase, row, rvalid, ti, args);
       else if constexpr (EPI == EPI_BIAS) epi_bias<T, TN, false>(tbase, row, rvalid, ti, args);
       else if constexpr (EPI == EPI_BIAS_WSCATTER) epi_bias<T, TN, true>(tbase, row, rvalid, ti, args);
       else if constexpr (EPI == EPI_PARTIAL) epi_partial(tbase, row, rvalid, ti, args, ti.n0 / TN);

@@ -139,16 +139,15 @@ cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const u
                         const int32_t* off, const uint8_t* w_codes, const uint8_t* w_tiles, const void* bias,
                         bool out_f32, void* out);
 
-// Training pass of the expert block (ffn_backward.cuh).  Activation: gate_lo = 0 for the
+// Training pass of the expert block (train_gemm.cuh, simt_train.cuh).  Activation: gate_lo = 0 for the
 // clipped SwiGLU; gate_lo = -inf, limit = inf, alpha = 1 for SiLU.
 struct Activation {
   float limit, alpha, gate_lo;
 };
-// gate/up projections of a bf16 layer storing gu [R, 2, F] and h [R, F]; w.b_gate / w.b_up may be null.
-cudaError_t expert_gateup_save(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
-                               const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
-                               void* h);
-// The whole training forward of an fp32 layer; each bias may be null.
+// The forward pass storing gu [R, 2, F], h [R, F] and y_perm [R, D]; each bias may be null.
+cudaError_t expert_train_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
+                              const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
+                              void* h, void* y_perm);
 cudaError_t expert_train_f32(const Launch& L, int64_t R, int D, int F, int E, const float* x_perm,
                              const int32_t* expert_off, const ExpertWeights& w, const Activation& act, float* gu,
                              float* h, float* y_perm);

@@ -874,14 +874,9 @@ moe_status_t moe_mxfp4_linear(int32_t G, int64_t R, int32_t N, int32_t K, const 
       moe::mx4_product(L, R, N, K, G, codes, tiles, group_off, w_codes, w_tiles, bias, out_f32 != 0, out));
 }
 
-size_t moe_expert_ffn_train_workspace_size(const moe_config_t* cfg, int64_t T) {
-  if (check_train(cfg, MOE_ACT_SWIGLU) != MOE_OK || !check_T(T, cfg->num_experts_per_tok)) return size_t(-1);
-  return align256(size_t(cfg->num_local_experts) * cfg->hidden_size * elem_size(cfg));
-}
-
 moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
                                   const int32_t* expert_off, const moe_expert_weights_t* weights, void* gu, void* h,
-                                  void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+                                  void* y_perm, void* stream) {
   const moe_status_t s = check_train(cfg, act);
   if (s != MOE_OK) return s;
   if (!check_T(T, cfg->num_experts_per_tok)) return MOE_ERR_INVALID_ARG;
@@ -894,23 +889,14 @@ moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t 
   const bool bf16 = cfg->dtype == MOE_BF16;
   const int D = cfg->hidden_size, F = cfg->intermediate_size, E = cfg->num_local_experts;
   const int64_t R = T * cfg->num_experts_per_tok;
-  moe::ExpertWeights w = to_internal(weights);
+  const moe::ExpertWeights w = to_internal(weights);
   const moe::Activation a = activation(cfg, act);
-  const size_t need = align256(size_t(E) * D * elem_size(cfg));
-  const bool zeros = bf16 && weights->b_down == nullptr;   // the down projection's epilogue reads a bias
-  if (zeros && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   Launch L;
   if (!get_launch(stream, &L)) return MOE_ERR_CUDA;
-  if (!bf16)
-    return cuda_status(moe::expert_train_f32(L, R, D, F, E, static_cast<const float*>(x_perm), expert_off, w, a,
-                                             static_cast<float*>(gu), static_cast<float*>(h),
-                                             static_cast<float*>(y_perm)));
-  if (zeros) {
-    if (cudaMemsetAsync(ws, 0, need, L.stream) != cudaSuccess) return MOE_ERR_CUDA;
-    w.b_down = ws;
-  }
-  if (moe::expert_gateup_save(L, R, D, F, E, x_perm, expert_off, w, a, gu, h) != cudaSuccess) return MOE_ERR_CUDA;
-  return cuda_status(moe::expert_down(L, true, R, D, F, E, h, expert_off, w, nullptr, nullptr, y_perm));
+  if (bf16) return cuda_status(moe::expert_train_bf16(L, R, D, F, E, x_perm, expert_off, w, a, gu, h, y_perm));
+  return cuda_status(moe::expert_train_f32(L, R, D, F, E, static_cast<const float*>(x_perm), expert_off, w, a,
+                                           static_cast<float*>(gu), static_cast<float*>(h),
+                                           static_cast<float*>(y_perm)));
 }
 
 size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T) {

@@ -1,6 +1,6 @@
 // The expert block's training pass for fp32 layers, in fp32 FMA (TF32 would truncate the
 // operands to 10 mantissa bits): the forward products and the three backward ones of
-// ffn_backward.cuh as one tiled kernel.
+// train_gemm.cuh as one tiled kernel.
 //
 // These layers are small, so a launch is a chain of K steps more than a rate: tiles of 32
 // rows (an expert often has fewer) x 64 columns (32 for the products with the longest K and
@@ -13,7 +13,7 @@
 // row; either way a thread takes 4 x 4 of it per four K steps with four 16-byte loads.
 #pragma once
 
-#include "ffn_backward.cuh"
+#include "train_gemm.cuh"
 
 namespace moe {
 

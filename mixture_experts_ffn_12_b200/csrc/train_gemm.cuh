@@ -1,8 +1,10 @@
-// Backward pass of the experts' gated feed-forward block, as grouped GEMMs on tcgen05.
+// Training pass of the experts' gated feed-forward block, as grouped GEMMs on tcgen05 (bf16).
 //
 // Forward (per expert e and row r): g = x Wg^T + bg, u = x Wu^T + bu, h = f(g') u',
 // y = h Wd^T + bd, with f(a) = a s(alpha a), s the sigmoid, and g' = clip(g, gate_lo, L),
-// u' = clip(u, -L, L) (SiLU: no clips, alpha = 1).  Given dy:
+// u' = clip(u, -L, L) (SiLU: no clips, alpha = 1):
+//   GATEUP  gu [R, 2, F] = (g, u) and h [R, F];   DOWN  y.
+// Backward, given dy:
 //   DH  dh = dy Wd;  dg = dh u' f'(g') [gate_lo <= g <= L],  du = dh f(g') [|u| <= L],
 //       f'(a) = s + alpha a s (1 - s)                                  -> dgu [R, 2, F]
 //   DX  dx = dg Wg + du Wu
@@ -14,10 +16,11 @@
 // tensor core reads directly (instruction descriptor transpose bits, 128-byte swizzle: 64
 // elements x 8 K-rows per 1024-byte atom) at the rate of K-major ones.  DW has both operands
 // MN-major, its K running over rows.  TMA brings [64 K-rows x 64 elements] boxes; nothing is
-// transposed in memory.  DH and DX put the weights in M (their output transposed, 256 output
-// columns a tile) and the expert's rows in N, split evenly into tiles of at most 256 in steps
-// of 16: a ragged expert wastes at most 15 rows of MMA work a tile, where rows in M would
-// round every expert up to 128 or 256.
+// transposed in memory.  All but DW put the weights in M (their output transposed, 256
+// output columns a tile) and the expert's rows in N, split evenly into tiles of at most 256
+// in steps of 16: a ragged expert wastes at most 15 rows of MMA work a tile, where rows in M
+// would round every expert up to 128 or 256.  GATEUP has two accumulators (gate and up of
+// the same 256 features) and tiles of at most 128 rows.
 
 // DW's K range is an expert's row range, of any length.  Its last block may reach into
 // rows of the next expert: whole 16-row MMA steps past the end are not issued, and the
@@ -50,75 +53,81 @@
 
 namespace moe {
 
-enum BwdKind : int { BWD_DH = 0, BWD_DX = 1, BWD_DW = 2 };
+enum TrainKind : int { TR_GATEUP = 0, TR_DOWN = 1, TR_DH = 2, TR_DX = 3, TR_DW = 4 };
 
-constexpr int kBwdBM = 256;          // M of a pair's tile, and the most rows in its N (DH, DX)
-constexpr int kBwdBK = 64;           // K per stage
-constexpr int kBwdStages = 6;
-constexpr int kBwdBox = 64 * 128;    // bytes of a [64 K-rows x 64 elements] box
-constexpr int kBwdOnesCol = 128;     // TMEM column of the bias sums inside an accumulator buffer
-constexpr int kBwdThreads = 384;
-constexpr int kBwdEpiWarps = 8;
-constexpr int kBwdSched = 4;         // tiles the scheduler is ahead
+constexpr int kTrBM = 256;           // M of a pair's tile
+constexpr int kTrBK = 64;           // K per stage
+constexpr int kTrBox = 64 * 128;    // bytes of a [64 K-rows x 64 elements] box
+constexpr int kTrOnesCol = 128;     // TMEM column of the bias sums inside an accumulator buffer
+constexpr int kTrUpCol = 128;        // GATEUP: TMEM column of the up accumulator
+constexpr int kTrThreads = 384;
+constexpr int kTrEpiWarps = 8;
+constexpr int kTrSched = 4;         // tiles the scheduler is ahead
 
 template <int KIND>
-struct BwdLayout {
-  static constexpr int A_BYTES = 2 * kBwdBox;
-  static constexpr int B_BYTES = 2 * kBwdBox;
+struct TrainLayout {
+  static constexpr int ROWS = KIND == TR_GATEUP ? 128 : 256;    // most rows in a tile's N (not DW)
+  static constexpr int NA = KIND == TR_GATEUP ? 2 : 1;          // A operands (and accumulators)
+  static constexpr bool A_KMAJOR = KIND == TR_GATEUP || KIND == TR_DOWN;
+  static constexpr int STAGES = KIND == TR_GATEUP ? 5 : 6;
+  static constexpr int A_BYTES = NA * 2 * kTrBox;
+  static constexpr int B_BYTES = ROWS / 2 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int ONES = KIND == BWD_DW ? 1024 : 0;   // 8 rows x 128 B of bf16 ones: half of N = 16
-  static constexpr int STAGING_WARP = KIND == BWD_DW ? 32 * 80 : 0;   // epilogue: 32 rows of 64 B + 16 B
-  static constexpr int STAGING = kBwdEpiWarps * STAGING_WARP;
+  static constexpr int ONES = KIND == TR_DW ? 1024 : 0;   // 8 rows x 128 B of bf16 ones: half of N = 16
+  static constexpr int STAGING_WARP = KIND == TR_DW ? 32 * 80 : 0;   // epilogue: 32 rows of 64 B + 16 B
+  static constexpr int STAGING = kTrEpiWarps * STAGING_WARP;
   static constexpr int EXTRA = 1024 + 3072;
-  static constexpr int SMEM = kBwdStages * STAGE_BYTES + ONES + STAGING + EXTRA;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + ONES + STAGING + EXTRA;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 // Column blocks of N columns: 1 or 2 units of 128 each (1 for the first one if `spare`), the
 // narrower ones first.
-__host__ __device__ constexpr int bwd_col_blocks(int N, bool spare) {
+__host__ __device__ constexpr int train_col_blocks(int N, bool spare) {
   return ((N + 127) / 128 + (spare ? 1 : 0) + 1) / 2;
 }
-struct BwdCols {
+struct TrainCols {
   int first, units;   // first column, number of 128-column units
 };
-__host__ __device__ inline BwdCols bwd_cols(int N, int blocks, int j) {
+__host__ __device__ inline TrainCols train_cols(int N, int blocks, int j) {
   const int n = (N + 127) / 128;
   const int q = n / blocks, narrow = blocks - n % blocks;
-  return BwdCols{128 * (j * q + (j > narrow ? j - narrow : 0)), q + (j >= narrow ? 1 : 0)};
+  return TrainCols{128 * (j * q + (j > narrow ? j - narrow : 0)), q + (j >= narrow ? 1 : 0)};
 }
 
-// One product of a launch.  DW: a, b[0] = the two row-major operands whose rows are summed
-// over.  DH: a = Wd, b = dy.  DX: a, a2 = Wg, Wu, b = dgu; b[q] has boxes of 64 K elements x
-// 32 (q + 1) rows.
+// One product of a launch.  DW: a, bw = the two row-major operands whose rows are summed
+// over.  Else a (and a2) = the weights, b = the rows: GATEUP Wg, Wu and x;  DOWN Wd and h;
+// DH Wd and dy;  DX Wg, Wu and dgu.  K-major operands have boxes of 64 K elements x 128
+// weight rows (a.single) or 32 (q + 1) rows (b[q]).
 // Two boxes of a K-rows x elements operand come in one copy: the matrix seen as {64 columns,
 // K rows, N / 64} (and groups), a box of 64 x 64 x 2 landing as consecutive [64 x 64] boxes.
 // Where the partial box of an N that is no multiple of 64 is met, and for one box alone, the
 // copies are single boxes.  (One TMA instruction costs the producer thread some 100 cycles.)
-struct BwdMaps {
+struct TrainMaps {
   CUtensorMap two, single;
 };
-struct BwdJob {
-  BwdMaps a, a2;
+struct TrainJob {
+  TrainMaps a, a2;
   union {
-    BwdMaps bw;         // DW
-    CUtensorMap b[4];   // DH, DX
+    TrainMaps bw;         // DW
+    CUtensorMap b[4];   // the others
   };
   void* out;
   void* bias_out;   // DW: [G, m] column sums of A, or null
-  int m, n;         // DW: rows and columns of the gradient;  DH, DX: m = columns of the output
+  const __nv_bfloat16 *bias0, *bias1;   // GATEUP (gate, up), DOWN: [G, m], or null
+  int m, n;         // DW: rows and columns of the gradient;  else m = columns of the output
   int nt;           // DW: column blocks
 };
 
 template <int KIND>
-struct BwdArgs {
-  BwdJob job[KIND == BWD_DW ? 3 : 1];
+struct TrainArgs {
+  TrainJob job[KIND == TR_DW ? 3 : 1];
   int num_jobs;
   const int32_t* group_off;   // [G+1]
   int num_groups;
   int m_total;                // R
-  int k_dim;                  // DH: D;  DX: F
-  const __nv_bfloat16* gu;    // DH: [R, 2, F]
+  int k_dim;                  // K (DX: of one half)
+  __nv_bfloat16* gu;          // GATEUP (written), DH: [R, 2, F]
   float limit, alpha, gate_lo;
   unsigned long long wait_limit_ns;
 };
@@ -139,16 +148,41 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const void* tmap, ui
       : "memory");
 }
 
-// K-rows x elements operand ("MN-major"), 128-byte swizzle: 64-element blocks kBwdBox bytes
+// K-rows x elements operand ("MN-major"), 128-byte swizzle: 64-element blocks kTrBox bytes
 // apart (leading offset), 8-row groups 1024 bytes apart (stride offset).
 __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kBwdBox >> 4) << 16;
+  d |= static_cast<uint64_t>(kTrBox >> 4) << 16;
   d |= static_cast<uint64_t>(1024 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
+}
+
+// A lane's values of one column in rows j (a) and j + 1 (b), rounded to bf16 and traded with
+// the neighbouring lane: the even lane gets both columns of row j, the odd one of row j + 1.
+__device__ __forceinline__ uint32_t trade_pair(float a, float b) {
+  const __nv_bfloat162 mine = __floats2bfloat162_rn(a, b);
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(&mine);
+  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
+  return (threadIdx.x & 1) ? __byte_perm(y, x, 0x7632) : __byte_perm(x, y, 0x5410);
+}
+// The way back: both columns of the lane's row to its own column in rows j and j + 1.
+__device__ __forceinline__ float2 untrade_pair(uint32_t x) {
+  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
+  const uint32_t z = (threadIdx.x & 1) ? __byte_perm(y, x, 0x7632) : __byte_perm(x, y, 0x5410);
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&z));
+}
+
+// v rounded to bf16, kept on its side of the bounds +-lim: the backward pass decides from the
+// stored value whether the clip let the gradient through, so rounding must not move it across.
+__device__ __forceinline__ float bf16_keep_side(float v, float lim) {
+  const float a = fabsf(v);
+  uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+  const bool over = a > lim;
+  if ((__bfloat162float(__ushort_as_bfloat16(b)) > lim) != over) b += over ? 1 : -1;
+  return copysignf(__bfloat162float(__ushort_as_bfloat16(b)), v);
 }
 
 // Derivatives of h = f(clip(g)) clip(u) times dh.  The clips pass the gradient at their ends.
@@ -161,27 +195,27 @@ __device__ __forceinline__ void act_grad(float dh, float g, float u, float limit
   du = (u >= -limit && u <= limit) ? dh * f : 0.0f;
 }
 
-struct BwdTile {
+struct TrainTile {
   int job, g;           // job -1: no more tiles
-  int m0;               // first row of the gradient (DW), first column of the output (DH, DX)
+  int m0;               // first row of the gradient (DW), first column of the output (others)
   int n0, units;        // DW: first column, 128-column units
   int n;                // MMA N
   int kb;               // 64-deep K blocks
-  int r0, rows;         // DW: the expert's rows;  DH, DX: the tile's
+  int r0, rows;         // DW: the expert's rows;  others: the tile's
   int sums;             // DW: bias gradients wanted of this tile
 };
 
 // DW: the last K block of the tile ends inside a 16-row MMA step.
-__device__ __forceinline__ bool bwd_ragged(const BwdTile& t) { return (t.rows & 15) != 0; }
+__device__ __forceinline__ bool train_ragged(const TrainTile& t) { return (t.rows & 15) != 0; }
 
 template <int KIND>
-__device__ __forceinline__ BwdTile bwd_tile(int i, const int* tile_off, const int* goff, const BwdArgs<KIND>& a) {
-  BwdTile t{};
-  if constexpr (KIND == BWD_DW) {
+__device__ __forceinline__ TrainTile train_tile(int i, const int* tile_off, const int* goff, const TrainArgs<KIND>& a) {
+  TrainTile t{};
+  if constexpr (KIND == TR_DW) {
     int mt, nt;
     for (;; ++t.job) {
       nt = a.job[t.job].nt;
-      mt = (a.job[t.job].m + kBwdBM - 1) / kBwdBM;
+      mt = (a.job[t.job].m + kTrBM - 1) / kTrBM;
       const int n = a.num_groups * mt * nt;
       if (i < n || t.job + 1 == a.num_jobs) break;
       i -= n;
@@ -194,18 +228,18 @@ __device__ __forceinline__ BwdTile bwd_tile(int i, const int* tile_off, const in
     const int rem = i - band * kBand * nt;
     const int rows = min(kBand, mt - band * kBand);
     const int nb = rem / rows;
-    t.m0 = (band * kBand + rem - nb * rows) * kBwdBM;
-    const BwdCols c = bwd_cols(a.job[t.job].n, nt, nb);
+    t.m0 = (band * kBand + rem - nb * rows) * kTrBM;
+    const TrainCols c = train_cols(a.job[t.job].n, nt, nb);
     t.n0 = c.first;
     t.units = c.units;
     t.n = 128 * c.units;
     t.r0 = goff[t.g];
     t.rows = max(0, goff[t.g + 1] - t.r0);
-    t.kb = (t.rows + kBwdBK - 1) / kBwdBK;
+    t.kb = (t.rows + kTrBK - 1) / kTrBK;
     t.sums = t.n0 == 0 && a.job[t.job].bias_out != nullptr ? 1 : 0;
   } else {
     // tiles of an expert: its row tiles fastest (they share the weight columns)
-    const int mt = (a.job[0].m + kBwdBM - 1) / kBwdBM;
+    const int mt = (a.job[0].m + kTrBM - 1) / kTrBM;
     int lo = 0, hi = a.num_groups;            // tile_off[lo] * mt <= i < tile_off[hi] * mt
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -216,12 +250,12 @@ __device__ __forceinline__ BwdTile bwd_tile(int i, const int* tile_off, const in
     i -= tile_off[lo] * mt;
     const int mb = i / rt, r = i - mb * rt;
     const int per = ((rows + rt - 1) / rt + 15) / 16 * 16;
-    t.m0 = mb * kBwdBM;
+    t.m0 = mb * kTrBM;
     t.r0 = goff[lo] + r * per;
     t.rows = min(per, rows - r * per);
     t.n = (t.rows + 15) / 16 * 16;
-    const int kb = (a.k_dim + kBwdBK - 1) / kBwdBK;
-    t.kb = KIND == BWD_DX ? 2 * kb : kb;
+    const int kb = (a.k_dim + kTrBK - 1) / kTrBK;
+    t.kb = KIND == TR_DX ? 2 * kb : kb;
   }
   return t;
 }
@@ -257,24 +291,24 @@ __device__ __forceinline__ void store_rows64(uint8_t* stage, T* out, size_t ldo,
 }
 
 template <int KIND, typename OutT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
-    ffn_backward_kernel(const __grid_constant__ BwdArgs<KIND> args) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
+    ffn_train_kernel(const __grid_constant__ TrainArgs<KIND> args) {
   pdl_enter();
-  using LY = BwdLayout<KIND>;
+  using LY = TrainLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ones = smem + kBwdStages * LY::STAGE_BYTES;
+  uint8_t* ones = smem + LY::STAGES * LY::STAGE_BYTES;
   uint8_t* staging = ones + LY::ONES;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + LY::STAGING);   // leader's: both CTAs' stage is in place
-  uint64_t* landed = full + kBwdStages;         // DW: a ragged tail's loads have landed in this CTA
-  uint64_t* empty = landed + kBwdStages;
-  uint64_t* tfull = empty + kBwdStages;
+  uint64_t* landed = full + LY::STAGES;         // DW: a ragged tail's loads have landed in this CTA
+  uint64_t* empty = landed + LY::STAGES;
+  uint64_t* tfull = empty + LY::STAGES;
   uint64_t* tempty = tfull + 2;                 // leader's
   uint64_t* sfull = tempty + 2;                 // scheduler ring
-  uint64_t* sempty = sfull + kBwdSched;
-  uint64_t* drain = sempty + kBwdSched;
-  BwdTile* ring = reinterpret_cast<BwdTile*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kBwdSched);
+  uint64_t* sempty = sfull + kTrSched;
+  uint64_t* drain = sempty + kTrSched;
+  TrainTile* ring = reinterpret_cast<TrainTile*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kTrSched);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* never_flag = abort_flag + 1;
   int* tile_off = never_flag + 1;              // [G+1]
@@ -287,18 +321,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
   const uint64_t lim = args.wait_limit_ns;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kBwdStages; ++s) {
+    for (int s = 0; s < LY::STAGES; ++s) {
       mbar_init(&full[s], 2);      // one arrival a CTA: its producer's, or its blanker's
       mbar_init(&landed[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kBwdEpiWarps);
+      mbar_init(&tempty[b], 2 * kTrEpiWarps);
     }
-    for (int q = 0; q < kBwdSched; ++q) {
+    for (int q = 0; q < kTrSched; ++q) {
       mbar_init(&sfull[q], 1);
-      mbar_init(&sempty[q], 1 + (rank == 0 ? 1 : 0) + kBwdEpiWarps + (KIND == BWD_DX ? 0 : 1));   // who reads a tile
+      mbar_init(&sempty[q], 1 + (rank == 0 ? 1 : 0) + kTrEpiWarps + (KIND == TR_DH || KIND == TR_DW ? 1 : 0));   // who reads a tile
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -307,15 +341,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    mx4_group_table<kBwdBM>(args.group_off, G, args.m_total, goff, tile_off);
+    mx4_group_table<LY::ROWS>(args.group_off, G, args.m_total, goff, tile_off);
     if (lane < args.num_jobs) {
       tma_prefetch_desc(&args.job[lane].a.single);
-      tma_prefetch_desc(KIND == BWD_DW ? &args.job[lane].bw.single : &args.job[lane].b[3]);
+      tma_prefetch_desc(KIND == TR_DW ? &args.job[lane].bw.single : &args.job[lane].b[0]);
     }
   } else if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
-  } else if (KIND == BWD_DW && warp < 6) {
+  } else if (KIND == TR_DW && warp < 6) {
     for (int i = threadIdx.x - 64; i < LY::ONES / 4; i += 128) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
   }
@@ -325,13 +359,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-  const int KB1 = (args.k_dim + kBwdBK - 1) / kBwdBK;   // DX: K blocks of one half
+  const int KB1 = (args.k_dim + kTrBK - 1) / kTrBK;   // DX: K blocks of one half
 
   // The next tile from the scheduler's ring; false when a wait gave up.  One thread, or a
   // whole warp (which then agrees on the answer).
-  auto next_tile = [&](int n, BwdTile& t, bool whole_warp) {
-    const int q = n % kBwdSched;
-    bool got = mbar_wait(&sfull[q], (n / kBwdSched) & 1, abort_flag, lim);
+  auto next_tile = [&](int n, TrainTile& t, bool whole_warp) {
+    const int q = n % kTrSched;
+    bool got = mbar_wait(&sfull[q], (n / kTrSched) & 1, abort_flag, lim);
     if (whole_warp) got = __all_sync(0xffffffffu, got);
     if (!got) return false;
     t = ring[q];
@@ -340,29 +374,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
     return true;
   };
   // A tile that the whole warp has read, as values the compiler knows to be the same in every lane.
-  auto uniform = [](BwdTile& t) {
+  auto uniform = [](TrainTile& t) {
     int* f = reinterpret_cast<int*>(&t);
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(BwdTile) / sizeof(int)); ++i) f[i] = __shfl_sync(0xffffffffu, f[i], 0);
+    for (int i = 0; i < static_cast<int>(sizeof(TrainTile) / sizeof(int)); ++i) f[i] = __shfl_sync(0xffffffffu, f[i], 0);
   };
   bool ok = true;
 
-  if (warp == 2 + kBwdEpiWarps) {
+  if (warp == 2 + kTrEpiWarps) {
     // ------------------------------------------------------------ scheduler
     if (lane == 0) {
       int total = 0;
-      if constexpr (KIND == BWD_DW) {
-        for (int j = 0; j < args.num_jobs; ++j) total += G * ((args.job[j].m + kBwdBM - 1) / kBwdBM) * args.job[j].nt;
+      if constexpr (KIND == TR_DW) {
+        for (int j = 0; j < args.num_jobs; ++j) total += G * ((args.job[j].m + kTrBM - 1) / kTrBM) * args.job[j].nt;
       } else {
-        total = tile_off[G] * ((args.job[0].m + kBwdBM - 1) / kBwdBM);
+        total = tile_off[G] * ((args.job[0].m + kTrBM - 1) / kTrBM);
       }
       int n = 0;
       for (int i = blockIdx.x >> 1;; i += gridDim.x >> 1, ++n) {
-        BwdTile t;
+        TrainTile t;
         t.job = -1;
-        if (i < total) t = bwd_tile<KIND>(i, tile_off, goff, args);
-        const int q = n % kBwdSched;
-        if (!mbar_wait(&sempty[q], ((n / kBwdSched) & 1) ^ 1, abort_flag, lim)) { ok = false; break; }
+        if (i < total) t = train_tile<KIND>(i, tile_off, goff, args);
+        const int q = n % kTrSched;
+        if (!mbar_wait(&sempty[q], ((n / kTrSched) & 1) ^ 1, abort_flag, lim)) { ok = false; break; }
         ring[q] = t;
         mbar_arrive(&sfull[q]);
         if (i >= total) break;
@@ -382,34 +416,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;         // stages counted on the leader's full
       uint32_t tails = 0, tail_par = 0, tail_uses = 0;     // stages counted on this CTA's landed
-      BwdTile ti;
+      TrainTile ti;
       for (int n = 0;; ++n) {
         if (!next_tile(n, ti, true)) { ok = false; break; }
         uniform(ti);
         if (ti.job < 0) break;
-        const BwdJob& jb = args.job[ti.job];
+        const TrainJob& jb = args.job[ti.job];
         const int a_row = ti.m0 + rank * 128;
         const bool a_two = a_row + 128 <= (jb.m & ~63) || (jb.m & 63) == 0;
         const int b_col = ti.n0 + rank * 64 * ti.units;                       // DW
         const bool b_two = ti.units == 2 && b_col + 128 <= (jb.n & ~63);
-        const int b_row = ti.r0 + rank * (ti.n / 2), q32 = (ti.n + 63) / 64;   // DH, DX: boxes of 32 rows
-        const uint32_t tx = LY::A_BYTES + (KIND == BWD_DW ? ti.units * kBwdBox : q32 * (kBwdBox / 2));
+        const int b_row = ti.r0 + rank * (ti.n / 2), q32 = (ti.n + 63) / 64;   // others: boxes of 32 rows
+        const uint32_t tx = LY::A_BYTES + (KIND == TR_DW ? ti.units * kTrBox : q32 * (kTrBox / 2));
         for (int kb = 0; kb < ti.kb; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim))) { ok = false; break; }
           uint8_t* sa = smem + s * LY::STAGE_BYTES;
           uint8_t* sb = sa + LY::A_BYTES;
           const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
-          if (KIND == BWD_DW && kb == ti.kb - 1 && bwd_ragged(ti)) {
+          if (KIND == TR_DW && kb == ti.kb - 1 && train_ragged(ti)) {
             // the blanker is told here, and passes the stage on to the leader
-            const int r = ti.r0 + kb * kBwdBK;
+            const int r = ti.r0 + kb * kTrBK;
             if (leader) {
               mbar_arrive_expect_tx(&landed[s], tx);
               if (b_two) tma_load_3d(sb, &jb.bw.two, &landed[s], 0, r, b_col / 64);
               else
-                for (int q = 0; q < ti.units; ++q) tma_load_2d(sb + q * kBwdBox, &jb.bw.single, &landed[s], b_col + 64 * q, r);
+                for (int q = 0; q < ti.units; ++q) tma_load_2d(sb + q * kTrBox, &jb.bw.single, &landed[s], b_col + 64 * q, r);
               if (a_two) tma_load_3d(sa, &jb.a.two, &landed[s], 0, r, a_row / 64);
               else
-                for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kBwdBox, &jb.a.single, &landed[s], a_row + 64 * q, r);
+                for (int q = 0; q < 2; ++q) tma_load_2d(sa + q * kTrBox, &jb.a.single, &landed[s], a_row + 64 * q, r);
             }
             issued &= ~(1u << s);   // its earlier loads have landed, or the slot were not free
             tails |= 1u << s;
@@ -419,30 +453,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
             if (leader) {
               if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * tx);
               else mbar_arrive_cluster(fb);
-              if constexpr (KIND == BWD_DW) {
-                const int r = ti.r0 + kb * kBwdBK;
+              if constexpr (KIND == TR_DW) {
+                const int r = ti.r0 + kb * kTrBK;
                 if (b_two) tma_load_3d_pair(sb, &jb.bw.two, fb, 0, r, b_col / 64);
                 else
-                  for (int q = 0; q < ti.units; ++q) tma_load_2d_pair(sb + q * kBwdBox, &jb.bw.single, fb, b_col + 64 * q, r);
+                  for (int q = 0; q < ti.units; ++q) tma_load_2d_pair(sb + q * kTrBox, &jb.bw.single, fb, b_col + 64 * q, r);
                 if (a_two) tma_load_3d_pair(sa, &jb.a.two, fb, 0, r, a_row / 64);
                 else
-                  for (int q = 0; q < 2; ++q) tma_load_2d_pair(sa + q * kBwdBox, &jb.a.single, fb, a_row + 64 * q, r);
+                  for (int q = 0; q < 2; ++q) tma_load_2d_pair(sa + q * kTrBox, &jb.a.single, fb, a_row + 64 * q, r);
               } else {
-                const int half = (KIND == BWD_DX && kb >= KB1) ? 1 : 0;
-                const int k0 = (kb - half * KB1) * kBwdBK;
-                const BwdMaps& ma = half ? jb.a2 : jb.a;
-                if (a_two) tma_load_4d_pair(sa, &ma.two, fb, 0, k0, a_row / 64, ti.g);
-                else
-                  for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * kBwdBox, &ma.single, fb, a_row + 64 * q, k0, ti.g);
-                if (KIND == BWD_DX) tma_load_3d_pair(sb, &jb.b[q32 - 1], fb, k0, half, b_row);
-                else tma_load_2d_pair(sb, &jb.b[q32 - 1], fb, k0, b_row);
+                if constexpr (LY::A_KMAJOR) {
+                  tma_load_3d_pair(sa, &jb.a.single, fb, kb * kTrBK, a_row, ti.g);
+                  if (LY::NA == 2) tma_load_3d_pair(sa + 2 * kTrBox, &jb.a2.single, fb, kb * kTrBK, a_row, ti.g);
+                  tma_load_2d_pair(sb, &jb.b[q32 - 1], fb, kb * kTrBK, b_row);
+                } else {
+                  const int half = (KIND == TR_DX && kb >= KB1) ? 1 : 0;
+                  const int k0 = (kb - half * KB1) * kTrBK;
+                  const TrainMaps& ma = half ? jb.a2 : jb.a;
+                  if (a_two) tma_load_4d_pair(sa, &ma.two, fb, 0, k0, a_row / 64, ti.g);
+                  else
+                    for (int q = 0; q < 2; ++q) tma_load_3d_pair(sa + q * kTrBox, &ma.single, fb, a_row + 64 * q, k0, ti.g);
+                  if (KIND == TR_DX) tma_load_3d_pair(sb, &jb.b[q32 - 1], fb, k0, half, b_row);
+                  else tma_load_2d_pair(sb, &jb.b[q32 - 1], fb, k0, b_row);
+                }
               }
             }
             issued |= 1u << s;
             issued_par = (issued_par & ~(1u << s)) | (ph << s);
           }
           __syncwarp();
-          if (++s == kBwdStages) { s = 0; ph ^= 1u; }
+          if (++s == LY::STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
       }
@@ -452,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
         // the peer's barrier cannot be polled from here: give loads in flight time to land
         for (int q = 0; q < 2000; ++q) __nanosleep(1000);
       }
-      for (int q = 0; leader && q < kBwdStages; ++q) {
+      for (int q = 0; leader && q < LY::STAGES; ++q) {
         if (rank == 0 && ((issued >> q) & 1u))
           if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
         if ((tails >> q) & 1u)
@@ -468,21 +508,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
     if (rank == 0) {
       const bool leader = elect_one();
       const uint32_t s_addr = smem_u32(smem);
-      const uint64_t a_desc = sw128_mnmajor_desc(s_addr);
-      const uint64_t b_desc = KIND == BWD_DW ? sw128_mnmajor_desc(s_addr + LY::A_BYTES) : sw128_kmajor_desc(s_addr + LY::A_BYTES);
+      const uint64_t a_desc = LY::A_KMAJOR ? sw128_kmajor_desc(s_addr) : sw128_mnmajor_desc(s_addr);
+      const uint64_t b_desc = KIND == TR_DW ? sw128_mnmajor_desc(s_addr + LY::A_BYTES) : sw128_kmajor_desc(s_addr + LY::A_BYTES);
       const uint64_t ones_desc = sw128_kmajor_desc(smem_u32(ones));
-      constexpr int kAStep = 2048 / 16, kBStep = KIND == BWD_DW ? 2048 / 16 : 32 / 16;   // of 16 K elements
-      const uint32_t idesc_ones = make_idesc(kBwdBM, 16, 1u) | (1u << 15);
+      constexpr int kAStep = LY::A_KMAJOR ? 32 / 16 : 2048 / 16, kBStep = KIND == TR_DW ? 2048 / 16 : 32 / 16;   // of 16 K
+      const uint32_t idesc_ones = make_idesc(kTrBM, 16, 1u) | (1u << 15);
       int s = 0;
       uint32_t ph = 0;
       bool issued_any = false;
-      BwdTile ti;
+      TrainTile ti;
       for (int n = 0;; ++n) {
         if (!next_tile(n, ti, true)) { ok = false; break; }
         uniform(ti);
         if (ti.job < 0) break;
-        const uint32_t idesc = make_idesc(kBwdBM, ti.n, 1u) | (1u << 15) | (KIND == BWD_DW ? 1u << 16 : 0u);
-        const bool sums = KIND == BWD_DW && ti.sums != 0;
+        const uint32_t idesc = make_idesc(kTrBM, ti.n, 1u) | (LY::A_KMAJOR ? 0u : 1u << 15) | (KIND == TR_DW ? 1u << 16 : 0u);
+        const bool sums = KIND == TR_DW && ti.sums != 0;
         const int acc = n & 1;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim))) { ok = false; break; }
@@ -492,24 +532,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
           tc_fence_after();
           const uint64_t so = static_cast<uint64_t>(s * (LY::STAGE_BYTES >> 4));
           const uint64_t ad = a_desc + so, bd = b_desc + so;
-          const int steps = KIND == BWD_DW ? min(kBwdBK / 16, (ti.rows - kb * kBwdBK + 15) / 16) : kBwdBK / 16;
+          const int steps = KIND == TR_DW ? min(kTrBK / 16, (ti.rows - kb * kTrBK + 15) / 16) : kTrBK / 16;
           if (leader) {
-            if (steps == kBwdBK / 16 && !sums) {
+            if (steps == kTrBK / 16 && !sums) {
 #pragma unroll
-              for (int kk = 0; kk < kBwdBK / 16; ++kk)
+              for (int kk = 0; kk < kTrBK / 16; ++kk) {
                 tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0 ? 1u : 0u);
+                if (LY::NA == 2)
+                  tc_mma_pair(d_tmem + kTrUpCol, ad + (2 * kTrBox >> 4) + kk * kAStep, bd + kk * kBStep, idesc,
+                              (kb | kk) != 0 ? 1u : 0u);
+              }
             } else {
               for (int kk = 0; kk < steps; ++kk) {
                 const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
                 tc_mma_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate);
-                if (sums) tc_mma_pair(d_tmem + kBwdOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
+                if (sums) tc_mma_pair(d_tmem + kTrOnesCol, ad + kk * kAStep, ones_desc, idesc_ones, accumulate);
               }
             }
             tc_commit_pair_mc(&empty[s], 0x3);
           }
           __syncwarp();
           issued_any = true;
-          if (++s == kBwdStages) { s = 0; ph ^= 1u; }
+          if (++s == LY::STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
         if (leader) tc_commit_pair_mc(&tfull[acc], 0x3);
@@ -527,21 +571,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 2 + kBwdEpiWarps) {
+  } else if (warp < 2 + kTrEpiWarps) {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     // Two warps share a TMEM lane quarter and take its column chunks in turn.
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    BwdTile ti;
+    TrainTile ti;
     for (int n = 0;; ++n) {
       if (!next_tile(n, ti, true)) { ok = false; break; }
       if (ti.job < 0) break;
-      const BwdJob& jb = args.job[ti.job];
+      const TrainJob& jb = args.job[ti.job];
       const int acc = n & 1;
       const int row0 = ti.m0 + rank * 128 + quarter * 32;   // of the warp's accumulator rows
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kAccStride);
-      if constexpr (KIND == BWD_DW) {
+      if constexpr (KIND == TR_DW) {
         constexpr int COLS = 64 / static_cast<int>(sizeof(OutT));
         uint8_t* stage = staging + (warp - 2) * LY::STAGING_WARP;
         const int rows = jb.m - row0, width = min(ti.n, jb.n - ti.n0);
@@ -564,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
         }
         if (half == 0 && ti.sums) {
           float b[8];
-          tmem_ld8(tbase + kBwdOnesCol, b);
+          tmem_ld8(tbase + kTrOnesCol, b);
           tmem_ld_wait();
           if (lane < rows) {
             const float sum = none ? 0.0f : b[0];
@@ -574,25 +618,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
           }
         }
       } else {
-        // lane = output column, accumulator column = row: each access of the warp is a
-        // 64-byte run of one row.  16 rows at a time; DH's g and u of the next 16 are on
-        // their way while these are computed, the first before the accumulator is complete.
+        // Lane = output column, accumulator column = row, 16 rows at a time.  Neighbouring
+        // lanes trade halves (trade_pair), so that the even one holds both columns of a row
+        // and the odd one both of the next: every access is four bytes a lane, 64-byte runs
+        // of two rows.  DH's g and u of the next 16 rows are on their way while these are
+        // computed, the first before the accumulator is complete.
         const int col = row0 + lane, M = jb.m;
-        const bool cvalid = col < M;
-        constexpr int kRowElems = KIND == BWD_DH ? 2 : 1;   // DH: [R, 2, F]
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + static_cast<size_t>(ti.r0) * kRowElems * M + col;
-        const __nv_bfloat16* gu = args.gu + static_cast<size_t>(ti.r0) * kRowElems * M + col;
+        const bool cvalid = col < M;                          // M is a multiple of 16: of both lanes
+        constexpr int kRowElems = KIND == TR_DH ? 2 : 1;      // DH: [R, 2, F]
         const size_t ld = static_cast<size_t>(kRowElems) * M;
-        const int rows = cvalid ? ti.rows : 0;
-        __nv_bfloat16 pg[16], pu[16];
+        const int odd = lane & 1;
+        const int rows = (cvalid ? ti.rows : 0) - odd;        // this lane's rows are j + odd
+        const size_t at = static_cast<size_t>(ti.r0) * ld + col + odd * (ld - 1);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + at;
+        const size_t gu_at = static_cast<size_t>(ti.r0) * 2 * M + col + odd * (2 * static_cast<size_t>(M) - 1);
+        __nv_bfloat16* gu = args.gu + gu_at;
+        float bias0 = 0.0f, bias1 = 0.0f;
+        if constexpr (LY::A_KMAJOR) {
+          const size_t bi = static_cast<size_t>(ti.g) * M + col;
+          if (cvalid && jb.bias0 != nullptr) bias0 = __bfloat162float(jb.bias0[bi]);
+          if (KIND == TR_GATEUP && cvalid && jb.bias1 != nullptr) bias1 = __bfloat162float(jb.bias1[bi]);
+        }
+        uint32_t pg[8], pu[8];
         auto fetch = [&](int c) {
-          if constexpr (KIND == BWD_DH) {
+          if constexpr (KIND == TR_DH) {
             const __nv_bfloat16* p = gu + c * ld;
 #pragma unroll
-            for (int j = 0; j < 16; ++j, p += ld)
-              if (c + j < rows) {
-                pg[j] = p[0];
-                pu[j] = p[M];
+            for (int j = 0; j < 8; ++j, p += 2 * ld)
+              if (c + 2 * j < rows) {
+                pg[j] = *reinterpret_cast<const uint32_t*>(p);
+                pu[j] = *reinterpret_cast<const uint32_t*>(p + M);
+              } else {
+                pg[j] = pu[j] = 0;
               }
           }
         };
@@ -604,29 +661,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
           float v[16];
           tmem_ld8(tbase + c, *reinterpret_cast<float(*)[8]>(v));
           tmem_ld8(tbase + c + 8, *reinterpret_cast<float(*)[8]>(v + 8));
-          tmem_ld_wait();
-          __nv_bfloat16* o = out + c * ld;
-          if constexpr (KIND == BWD_DH) {
-            uint32_t d[16];
+          if constexpr (KIND == TR_GATEUP) {
+            float u[16];
+            tmem_ld8(tbase + kTrUpCol + c, *reinterpret_cast<float(*)[8]>(u));
+            tmem_ld8(tbase + kTrUpCol + c + 8, *reinterpret_cast<float(*)[8]>(u + 8));
+            tmem_ld_wait();
+            __nv_bfloat16* o = out + c * ld;
+            __nv_bfloat16* p = gu + c * 2 * ld;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float dg, du;
-              act_grad(v[j], __bfloat162float(pg[j]), __bfloat162float(pu[j]), args.limit, args.alpha, args.gate_lo,
-                       dg, du);
-              const __nv_bfloat162 both = __floats2bfloat162_rn(dg, du);
-              d[j] = *reinterpret_cast<const uint32_t*>(&both);
+            for (int j = 0; j < 16; j += 2, o += 2 * ld, p += 4 * ld) {
+              float h[2], g[2], w[2];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float gv = v[j + q] + bias0, uv = u[j + q] + bias1;
+                const float gc = fminf(fmaxf(gv, args.gate_lo), args.limit);
+                const float uc = fminf(fmaxf(uv, -args.limit), args.limit);
+                h[q] = __fdividef(gc, 1.0f + __expf(-args.alpha * gc)) * uc;
+                g[q] = bf16_keep_side(gv, args.limit);
+                w[q] = bf16_keep_side(uv, args.limit);
+              }
+              const uint32_t ph = trade_pair(h[0], h[1]), pgv = trade_pair(g[0], g[1]), puv = trade_pair(w[0], w[1]);
+              if (c + j < rows) {
+                *reinterpret_cast<uint32_t*>(o) = ph;
+                *reinterpret_cast<uint32_t*>(p) = pgv;
+                *reinterpret_cast<uint32_t*>(p + M) = puv;
+              }
+            }
+          } else if constexpr (KIND == TR_DH) {
+            tmem_ld_wait();
+            uint32_t dgs[8], dus[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 g = untrade_pair(pg[j]), u = untrade_pair(pu[j]);
+              float dg0, du0, dg1, du1;
+              act_grad(v[2 * j], g.x, u.x, args.limit, args.alpha, args.gate_lo, dg0, du0);
+              act_grad(v[2 * j + 1], g.y, u.y, args.limit, args.alpha, args.gate_lo, dg1, du1);
+              dgs[j] = trade_pair(dg0, dg1);
+              dus[j] = trade_pair(du0, du1);
             }
             fetch(c + 32);
+            __nv_bfloat16* o = out + c * ld;
 #pragma unroll
-            for (int j = 0; j < 16; ++j, o += ld)
-              if (c + j < rows) {
-                o[0] = __ushort_as_bfloat16(static_cast<uint16_t>(d[j]));
-                o[M] = __ushort_as_bfloat16(static_cast<uint16_t>(d[j] >> 16));
+            for (int j = 0; j < 8; ++j, o += 2 * ld)
+              if (c + 2 * j < rows) {
+                *reinterpret_cast<uint32_t*>(o) = dgs[j];
+                *reinterpret_cast<uint32_t*>(o + M) = dus[j];
               }
           } else {
+            tmem_ld_wait();
+            __nv_bfloat16* o = out + c * ld;
 #pragma unroll
-            for (int j = 0; j < 16; ++j, o += ld)
-              if (c + j < rows) o[0] = __float2bfloat16_rn(v[j]);
+            for (int j = 0; j < 16; j += 2, o += 2 * ld) {
+              const uint32_t both = trade_pair(v[j] + bias0, v[j + 1] + bias0);
+              if (c + j < rows) *reinterpret_cast<uint32_t*>(o) = both;
+            }
           }
         }
       }
@@ -638,10 +726,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
       *abort_flag = 1;
       flag_error(DEVERR_TIMEOUT);
     }
-  } else if (KIND == BWD_DH) {
+  } else if (KIND == TR_DH) {
     // ------------------------------------------------------------ prefetcher
     // g and u of coming tiles into the L2: the epilogue's loads look only 16 rows ahead.
-    BwdTile ti;
+    TrainTile ti;
     for (int n = 0;; ++n) {
       if (!next_tile(n, ti, true)) { ok = false; break; }
       if (ti.job < 0) break;
@@ -655,32 +743,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
       *abort_flag = 1;
       flag_error(DEVERR_TIMEOUT);
     }
-  } else if (KIND == BWD_DW) {
+  } else if (KIND == TR_DW) {
     // ------------------------------------------------------------ blanker (both CTAs)
     // Blanks the rows between the end of an expert and the end of its last 16-row step in
     // this CTA's operands, then makes the CTA's arrival on the leader's full barrier (the
     // proxy fence publishes the writes to the tensor core, as in grouped_gemm_pair_mx.cuh).
     int s = 0;
     uint32_t uses = 0;
-    BwdTile ti;
+    TrainTile ti;
     for (int n = 0;; ++n) {
       if (!next_tile(n, ti, true)) { ok = false; break; }
       if (ti.job < 0) break;
-      if (ti.kb > 0 && bwd_ragged(ti)) {
-        const int q = (s + ti.kb - 1) % kBwdStages;
+      if (ti.kb > 0 && train_ragged(ti)) {
+        const int q = (s + ti.kb - 1) % LY::STAGES;
         if (!__all_sync(0xffffffffu, mbar_wait(&landed[q], (uses >> q) & 1u, abort_flag, lim))) { ok = false; break; }
         uses ^= 1u << q;
-        const int valid = ti.rows - (ti.kb - 1) * kBwdBK;
+        const int valid = ti.rows - (ti.kb - 1) * kTrBK;
         uint8_t* st = smem + q * LY::STAGE_BYTES + valid * 128;
         const int pieces = (16 - (valid & 15)) * 8;
         for (int box = 0; box < 2 + ti.units; ++box)
           for (int p = lane; p < pieces; p += 32)
-            *reinterpret_cast<uint4*>(st + box * kBwdBox + p * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(st + box * kTrBox + p * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();   // read by the tensor core (async proxy)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(full_leader + static_cast<uint32_t>(q) * 8u);
       }
-      s = (s + ti.kb) % kBwdStages;
+      s = (s + ti.kb) % LY::STAGES;
     }
     if (!ok) {
       *abort_flag = 1;
@@ -694,78 +782,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBwdThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// combine, backward: dy_perm[row(t, j)] = w[t, j] dy[t], dw[t, j] = dy[t] . y_perm[row(t, j)]
-// ---------------------------------------------------------------------------
-// One CTA a token, as wide as its row where it can be (D / 8 threads), so that all k + 1
-// loads of a thread are in flight at once: dy[t] is read once and meets its k rows.  Bound by
-// memory, (1 + 2 k) D elements a token.  The dot products are summed per thread, then over
-// the warp and the CTA's warps in a fixed order.  KM = 4 or 8 >= k: registers for k rows.
-constexpr int kCombineBwdThreads = 384;   // at most
-template <typename T, int KM>
-__global__ void __launch_bounds__(kCombineBwdThreads)
-    combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ y_perm,
-                            const int32_t* __restrict__ row_of_slot, const float* __restrict__ w, int Tn, int k, int D,
-                            T* __restrict__ dy_perm, float* __restrict__ dw) {
-  pdl_enter();
-  __shared__ float part[kCombineBwdThreads / 32][KM];
-  constexpr int kWords = sizeof(T) / 2;   // 16-byte words of 8 elements
-  const int t = blockIdx.x;
-  const int R = Tn * k;
-  int row[KM];
-  float wt[KM], acc[KM];
-#pragma unroll
-  for (int j = 0; j < KM; ++j) {
-    row[j] = j < k ? row_of_slot[static_cast<size_t>(t) * k + j] : -1;
-    wt[j] = j < k ? w[static_cast<size_t>(t) * k + j] : 0.0f;
-    acc[j] = 0.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < KM; ++j)
-    if (j < k && (row[j] < 0 || row[j] >= R)) {
-      if (threadIdx.x == 0) flag_error(DEVERR_BOUNDS);
-      row[j] = -1;
-    }
-  for (int c = threadIdx.x * 8; c < D; c += blockDim.x * 8) {
-    uint4 rd[kWords], ry[KM][kWords];
-#pragma unroll
-    for (int q = 0; q < kWords; ++q) rd[q] = reinterpret_cast<const uint4*>(dy + static_cast<size_t>(t) * D + c)[q];
-#pragma unroll
-    for (int j = 0; j < KM; ++j)
-      if (row[j] >= 0)
-#pragma unroll
-        for (int q = 0; q < kWords; ++q)
-          ry[j][q] = reinterpret_cast<const uint4*>(y_perm + static_cast<size_t>(row[j]) * D + c)[q];
-    float d[8];
-    unpack8<T>(rd, d);
-#pragma unroll
-    for (int j = 0; j < KM; ++j) {
-      if (row[j] < 0) continue;
-      float y[8], o[8];
-      unpack8<T>(ry[j], y);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        acc[j] = fmaf(d[q], y[q], acc[j]);
-        o[q] = wt[j] * d[q];
-      }
-      store8<T>(dy_perm + static_cast<size_t>(row[j]) * D + c, o);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < KM; ++j) {
-    if (j >= k) break;
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = acc[j];
-  }
-  __syncthreads();
-  if (threadIdx.x < k) {
-    float s = 0.0f;
-    for (int q = 0; q < static_cast<int>(blockDim.x) / 32; ++q) s += part[q][threadIdx.x];
-    dw[static_cast<size_t>(t) * k + threadIdx.x] = s;
   }
 }
 

@@ -2,10 +2,11 @@
 // Host side of the MXFP4 product and of the expert block's training pass: tensor maps and
 // launches (tensor maps as in gemm_launch.cuh: boxes of 128 bytes x rows, 128-byte swizzle,
 // zeros out of range).
-#include "ffn_backward.cuh"
+#include "combine_backward.cuh"
 #include "gemm_launch.cuh"
 #include "grouped_gemm_mx4.cuh"
 #include "simt_train.cuh"
+#include "train_gemm.cuh"
 
 namespace moe {
 
@@ -39,9 +40,9 @@ static cudaError_t make_tmap_bytes(CUtensorMap* m, const void* ptr, uint64_t row
 }
 
 // bf16 rows [groups, rows, cols] that lie ld elements apart (groups 0: one matrix), as a
-// K-rows x elements operand (ffn_backward.cuh): boxes of 64 columns x 64 rows, alone and in
+// K-rows x elements operand (train_gemm.cuh): boxes of 64 columns x 64 rows, alone and in
 // pairs (only where the matrix has a whole box: below 64 columns no copy takes pairs).
-static cudaError_t make_bwd_maps(BwdMaps* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld,
+static cudaError_t make_mn_maps(TrainMaps* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld,
                                  uint64_t groups) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
@@ -114,47 +115,21 @@ cudaError_t mx4_product(const Launch& L, int64_t R, int N, int K, int G, const u
 // ---------------------------------------------------------------------------
 // expert block, training pass
 // ---------------------------------------------------------------------------
-cudaError_t expert_gateup_save(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
-                               const int32_t* expert_off, const ExpertWeights& w, const Activation& act, void* gu,
-                               void* h) {
-  GemmArgs a = base_args(L);
-  a.group_off = expert_off;
-  a.num_groups = E;
-  a.m_total = static_cast<int>(R);
-  a.n_out = F;
-  a.k_dim = D;
-  a.bias0 = w.b_gate;
-  a.bias1 = w.b_up;
-  a.limit = act.limit;
-  a.alpha = act.alpha;
-  a.gate_lo = act.gate_lo;
-  a.out = h;
-  a.ldo = F;
-  a.gu = gu;
-  CUtensorMap ta, tg, tu;
-  cudaError_t e;
-  if ((e = make_tmap(&ta, x_perm, false, D, R, 0, kBM)) != cudaSuccess) return e;
-  if ((e = make_tmap(&tg, w.w_gate, false, D, F, E, kTNGateUp)) != cudaSuccess) return e;
-  if ((e = make_tmap(&tu, w.w_up, false, D, F, E, kTNGateUp)) != cudaSuccess) return e;
-  const int64_t tiles = max_row_blocks(R, E) * ((F + kTNGateUp - 1) / kTNGateUp);
-  return launch<__nv_bfloat16, kTNGateUp, 2, EPI_SWIGLU_SAVE, kStages>(L, ta, tg, tu, a, tiles);
-}
-
 template <int KIND, typename OutT>
-static cudaError_t launch_backward(const Launch& L, const BwdArgs<KIND>& args, int64_t max_tiles) {
-  auto kern = ffn_backward_kernel<KIND, OutT>;   // clusters of two CTAs
-  const cudaError_t e = allow_smem<ffn_backward_kernel<KIND, OutT>>(BwdLayout<KIND>::SMEM);
+static cudaError_t launch_train(const Launch& L, const TrainArgs<KIND>& args, int64_t max_tiles) {
+  auto kern = ffn_train_kernel<KIND, OutT>;   // clusters of two CTAs
+  const cudaError_t e = allow_smem<ffn_train_kernel<KIND, OutT>>(TrainLayout<KIND>::SMEM);
   if (e != cudaSuccess) return e;
-  pdl_launch(kern, dim3(2 * static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms / 2))), dim3(kBwdThreads),
-             BwdLayout<KIND>::SMEM, L.stream, args);
+  pdl_launch(kern, dim3(2 * static_cast<int>(std::min<int64_t>(max_tiles, L.num_sms / 2))), dim3(kTrThreads),
+             TrainLayout<KIND>::SMEM, L.stream, args);
   count_launch();
   return cudaGetLastError();
 }
 
 template <int KIND>
-static BwdArgs<KIND> backward_args(const Launch& L, int64_t R, int E, int k_dim, const int32_t* off,
+static TrainArgs<KIND> train_args(const Launch& L, int64_t R, int E, int k_dim, const int32_t* off,
                                    const Activation& act) {
-  BwdArgs<KIND> a{};
+  TrainArgs<KIND> a{};
   a.num_jobs = 1;
   a.group_off = off;
   a.num_groups = E;
@@ -167,7 +142,46 @@ static BwdArgs<KIND> backward_args(const Launch& L, int64_t R, int E, int k_dim,
   return a;
 }
 
-static int64_t bwd_row_tiles(int64_t R, int E) { return (R + kBwdBM - 1) / kBwdBM + E; }
+// Row tiles of at most `most` rows that R rows of E experts can take.
+static int64_t train_row_tiles(int64_t R, int E, int most) { return (R + most - 1) / most + E; }
+static int64_t train_col_tiles(int n) { return (n + kTrBM - 1) / kTrBM; }
+
+// Rows [R, K] in bf16 as the N operand: boxes of 64 elements x 32, 64, .. rows.
+static cudaError_t make_row_maps(CUtensorMap* m, int count, const void* ptr, uint64_t K, uint64_t R) {
+  for (int q = 0; q < count; ++q) {
+    const cudaError_t e = make_tmap(&m[q], ptr, false, K, R, 0, 32 * (q + 1));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t expert_train_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
+                              const int32_t* off, const ExpertWeights& w, const Activation& act, void* gu, void* h,
+                              void* y_perm) {
+  cudaError_t e;
+  {
+    TrainArgs<TR_GATEUP> a = train_args<TR_GATEUP>(L, R, E, D, off, act);
+    TrainJob& j = a.job[0];
+    if ((e = make_tmap(&j.a.single, w.w_gate, false, D, F, E, 128)) != cudaSuccess) return e;
+    if ((e = make_tmap(&j.a2.single, w.w_up, false, D, F, E, 128)) != cudaSuccess) return e;
+    if ((e = make_row_maps(j.b, 2, x_perm, D, R)) != cudaSuccess) return e;
+    j.out = h;
+    j.bias0 = static_cast<const __nv_bfloat16*>(w.b_gate);
+    j.bias1 = static_cast<const __nv_bfloat16*>(w.b_up);
+    j.m = F;
+    a.gu = static_cast<__nv_bfloat16*>(gu);
+    if ((e = launch_train<TR_GATEUP, __nv_bfloat16>(L, a, train_row_tiles(R, E, 128) * train_col_tiles(F))) != cudaSuccess)
+      return e;
+  }
+  TrainArgs<TR_DOWN> a = train_args<TR_DOWN>(L, R, E, F, off, act);
+  TrainJob& j = a.job[0];
+  if ((e = make_tmap(&j.a.single, w.w_down, false, F, D, E, 128)) != cudaSuccess) return e;
+  if ((e = make_row_maps(j.b, 4, h, F, R)) != cudaSuccess) return e;
+  j.out = y_perm;
+  j.bias0 = static_cast<const __nv_bfloat16*>(w.b_down);
+  j.m = D;
+  return launch_train<TR_DOWN, __nv_bfloat16>(L, a, train_row_tiles(R, E, 256) * train_col_tiles(D));
+}
 
 static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
                                         const int32_t* off, const ExpertWeights& w, const Activation& act,
@@ -176,49 +190,48 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   cudaError_t e;
   __nv_bfloat16* dg = static_cast<__nv_bfloat16*>(dgu);
   if (dx != nullptr || gr.w_gate != nullptr || gr.w_up != nullptr) {
-    BwdArgs<BWD_DH> a = backward_args<BWD_DH>(L, R, E, D, off, act);
-    BwdJob& j = a.job[0];
-    if ((e = make_bwd_maps(&j.a, w.w_down, F, D, F, E)) != cudaSuccess) return e;
-    for (int q = 0; q < 4; ++q)
-      if ((e = make_tmap(&j.b[q], dy, false, D, R, 0, 32 * (q + 1))) != cudaSuccess) return e;
+    TrainArgs<TR_DH> a = train_args<TR_DH>(L, R, E, D, off, act);
+    TrainJob& j = a.job[0];
+    if ((e = make_mn_maps(&j.a, w.w_down, F, D, F, E)) != cudaSuccess) return e;
+    if ((e = make_row_maps(j.b, 4, dy, D, R)) != cudaSuccess) return e;
     j.out = dgu;
     j.m = F;
-    a.gu = static_cast<const __nv_bfloat16*>(gu);
-    if ((e = launch_backward<BWD_DH, __nv_bfloat16>(L, a, bwd_row_tiles(R, E) * ((F + kBwdBM - 1) / kBwdBM))) != cudaSuccess)
+    a.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));   // read only
+    if ((e = launch_train<TR_DH, __nv_bfloat16>(L, a, train_row_tiles(R, E, 256) * train_col_tiles(F))) != cudaSuccess)
       return e;
   }
   if (dx != nullptr) {
-    BwdArgs<BWD_DX> a = backward_args<BWD_DX>(L, R, E, F, off, act);
-    BwdJob& j = a.job[0];
-    if ((e = make_bwd_maps(&j.a, w.w_gate, D, F, D, E)) != cudaSuccess) return e;
-    if ((e = make_bwd_maps(&j.a2, w.w_up, D, F, D, E)) != cudaSuccess) return e;
+    TrainArgs<TR_DX> a = train_args<TR_DX>(L, R, E, F, off, act);
+    TrainJob& j = a.job[0];
+    if ((e = make_mn_maps(&j.a, w.w_gate, D, F, D, E)) != cudaSuccess) return e;
+    if ((e = make_mn_maps(&j.a2, w.w_up, D, F, D, E)) != cudaSuccess) return e;
     for (int q = 0; q < 4; ++q)
       if ((e = make_tmap_halves(&j.b[q], dgu, F, R, 32 * (q + 1))) != cudaSuccess) return e;
     j.out = dx;
     j.m = D;
-    if ((e = launch_backward<BWD_DX, __nv_bfloat16>(L, a, bwd_row_tiles(R, E) * ((D + kBwdBM - 1) / kBwdBM))) != cudaSuccess)
+    if ((e = launch_train<TR_DX, __nv_bfloat16>(L, a, train_row_tiles(R, E, 256) * train_col_tiles(D))) != cudaSuccess)
       return e;
   }
-  BwdArgs<BWD_DW> a = backward_args<BWD_DW>(L, R, E, 0, off, act);
+  TrainArgs<TR_DW> a = train_args<TR_DW>(L, R, E, 0, off, act);
   a.num_jobs = 0;
   int64_t tiles = 0;
   auto add = [&](void* out, void* bias_out, const void* pa, int m, int64_t lda, const void* pb, int n) {
     if (out == nullptr) return cudaSuccess;
-    BwdJob& j = a.job[a.num_jobs++];
+    TrainJob& j = a.job[a.num_jobs++];
     j.out = out;
     j.bias_out = bias_out;
     j.m = m;
     j.n = n;
-    j.nt = bwd_col_blocks(n, bias_out != nullptr);
-    tiles += int64_t(E) * ((m + kBwdBM - 1) / kBwdBM) * j.nt;
-    const cudaError_t r = make_bwd_maps(&j.a, pa, m, R, lda, 0);
-    return r != cudaSuccess ? r : make_bwd_maps(&j.bw, pb, n, R, n, 0);
+    j.nt = train_col_blocks(n, bias_out != nullptr);
+    tiles += int64_t(E) * (train_col_tiles(m)) * j.nt;
+    const cudaError_t r = make_mn_maps(&j.a, pa, m, R, lda, 0);
+    return r != cudaSuccess ? r : make_mn_maps(&j.bw, pb, n, R, n, 0);
   };
   if ((e = add(gr.w_down, gr.b_down, dy, D, D, h, F)) != cudaSuccess) return e;
   if ((e = add(gr.w_gate, gr.b_gate, dg, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
   if ((e = add(gr.w_up, gr.b_up, dg + F, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
   if (a.num_jobs == 0) return cudaSuccess;
-  return grad_f32 ? launch_backward<BWD_DW, float>(L, a, tiles) : launch_backward<BWD_DW, __nv_bfloat16>(L, a, tiles);
+  return grad_f32 ? launch_train<TR_DW, float>(L, a, tiles) : launch_train<TR_DW, __nv_bfloat16>(L, a, tiles);
 }
 
 // ---------------------------------------------------------------------------
