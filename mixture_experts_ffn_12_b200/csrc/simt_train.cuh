@@ -2,13 +2,16 @@
 // operands to 10 mantissa bits): the forward products and the three backward ones of
 // train_gemm.cuh as one tiled kernel.
 //
-// These layers are small, so a launch is a chain of K steps more than a rate: tiles of 32
+// These layers are small, so a launch is a chain of K steps more than a rate.  Tiles of 32
 // rows (an expert often has fewer) x 64 columns (32 for the products with the longest K and
-// the fewest columns), 4 x 4 outputs a thread, a three-deep ring of cp.async copies of 32 K
-// elements, so that no step waits for the load it has just issued, and four (eight) groups
-// of threads that each take 8 (4) of a step's 32 K elements and add up at the end in a fixed
+// the fewest columns), 4 x 4 outputs a thread, a three-deep ring of cp.async copies of 32
+// (64) K elements, so that no step waits for the load it has just issued, and four (eight)
+// groups of threads that each take a part of a step's K and add up at the end in a fixed
 // order: one group alone leaves a scheduler one warp, which issues every third cycle
-// (gate/up of 128 rows, D = 256, F = 512: 27 us; with four groups 18 us).  An operand tile is kept in the order in which it lies in memory,
+// (gate/up of 128 rows, D = 256, F = 512: 27 us; with four groups 18 us).  The weight
+// gradients, whose K is an expert's few rows, are the other way about: few steps and many
+// outputs, one group and tiles of 64 x 128 (32 x 64 with four groups: 3072 CTAs of one
+// step each, 25 us).  An operand tile is kept in the order in which it lies in memory,
 // [row][K] (16-byte pieces along K) or [K][row] (along the rows), with 16 bytes of padding a
 // row; either way a thread takes 4 x 4 of it per four K steps with four 16-byte loads.
 #pragma once
@@ -19,7 +22,7 @@ namespace moe {
 
 enum SimtKind : int { SIMT_GATEUP = 0, SIMT_DOWN = 1, SIMT_DH = 2, SIMT_DX = 3, SIMT_DW = 4 };
 
-constexpr int kStM = 32, kStK = 32, kStStages = 3, kStThreads = 512;
+constexpr int kStStages = 3, kStThreads = 512;
 
 struct SimtJob {
   const float *a, *b0, *b1;   // GATEUP: b0, b1 = Wg, Wu;  DX: b0 then b1 along K
@@ -40,7 +43,10 @@ struct SimtTrainArgs {
 
 template <int KIND>
 struct SimtShape {
-  static constexpr int kStN = (KIND == SIMT_DOWN || KIND == SIMT_DX) ? 32 : 64;   // columns of a tile
+  static constexpr bool kLongK = KIND == SIMT_DOWN || KIND == SIMT_DX;
+  static constexpr int kStM = KIND == SIMT_DW ? 64 : 32;                     // rows of a tile
+  static constexpr int kStN = KIND == SIMT_DW ? 128 : kLongK ? 32 : 64;      // columns
+  static constexpr int kStK = kLongK ? 64 : 32;                              // K of a step
   static constexpr int kTX = kStN / 4, kPer = kTX * (kStM / 4), kStGroups = kStThreads / kPer;
   static constexpr bool kAK = KIND != SIMT_DW;                             // A tile [row][K]
   static constexpr bool kBK = KIND == SIMT_GATEUP || KIND == SIMT_DOWN;    // B tile [column][K]
@@ -63,7 +69,7 @@ template <int KIND>
 __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainArgs args) {
   pdl_enter();
   using S = SimtShape<KIND>;
-  constexpr int kStN = S::kStN, kStGroups = S::kStGroups;
+  constexpr int kStM = S::kStM, kStN = S::kStN, kStK = S::kStK, kStGroups = S::kStGroups;
   extern __shared__ __align__(16) float ring[];
   constexpr int kTable = KIND == SIMT_DW ? 1 : kMaxGroups + 1;
   __shared__ int goff[kTable], toff[kTable];
@@ -197,9 +203,9 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
     }
   }
 
-  // the groups' sums through the ring; group r then finishes row r of each thread's four
-  __syncthreads();
+  // the groups' sums through the ring; a group then finishes one row of each thread's four
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
   auto slot = [&](int group, int b, int r) { return ring + (((group * S::kNB + b) * 4 + r) * S::kPer + t) * 4; };
 #pragma unroll
   for (int b = 0; b < S::kNB; ++b)
@@ -209,8 +215,7 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
   if (KIND == SIMT_DW && tx == 0)
     for (int r = 0; r < 4; ++r) sums[grp][ty * 4 + r] = sum[r];
   __syncthreads();
-  if (grp < 4) {
-    const int r = grp;
+  for (int r = grp; r < 4; r += kStGroups) {   // group r (one group: all four rows)
     float tot[S::kNB][4] = {};
 #pragma unroll
     for (int b = 0; b < S::kNB; ++b)
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
         tot[b][3] += v.w;
       }
     const int row = m0 + ty * 4 + r;
-    if (row >= m_end) return;
+    if (row >= m_end) continue;
     const size_t orow = KIND == SIMT_DW ? static_cast<size_t>(g) * jb.m + row : row;
     if (KIND == SIMT_DW && jb.bias_out != nullptr && n0 == 0 && tx == 0) {
       float s = 0.0f;

@@ -263,7 +263,7 @@ static cudaError_t launch_simt(const Launch& L, const SimtTrainArgs& args, dim3 
 cudaError_t expert_train_f32(const Launch& L, int64_t R, int D, int F, int E, const float* x_perm,
                              const int32_t* off, const ExpertWeights& w, const Activation& act, float* gu, float* h,
                              float* y_perm) {
-  const unsigned row_tiles = simt_blocks(R, kStM) + E;
+  const unsigned row_tiles = simt_blocks(R, SimtShape<SIMT_GATEUP>::kStM) + E;
   SimtTrainArgs a = simt_args(R, E, off, act);
   auto f = [](const void* p) { return static_cast<const float*>(p); };
   a.gu_out = gu;
@@ -278,7 +278,7 @@ static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F,
                                        const int32_t* off, const ExpertWeights& w, const Activation& act,
                                        const float* gu, const float* h, const float* dy, float* dgu, float* dx,
                                        const ExpertGrads& gr) {
-  const unsigned row_tiles = simt_blocks(R, kStM) + E;
+  const unsigned row_tiles = simt_blocks(R, SimtShape<SIMT_GATEUP>::kStM) + E;
   SimtTrainArgs a = simt_args(R, E, off, act);
   auto f = [](const void* p) { return static_cast<const float*>(p); };
   cudaError_t e;
@@ -303,7 +303,7 @@ static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F,
   add(gr.w_gate, gr.b_gate, dgu, F, 2 * F, x_perm, D);
   add(gr.w_up, gr.b_up, dgu + F, F, 2 * F, x_perm, D);
   if (jobs == 0) return cudaSuccess;
-  return launch_simt<SIMT_DW>(L, a, dim3(simt_blocks(most_m, kStM), simt_blocks(most_n, SimtShape<SIMT_DW>::kStN), jobs * E));
+  return launch_simt<SIMT_DW>(L, a, dim3(simt_blocks(most_m, SimtShape<SIMT_DW>::kStM), simt_blocks(most_n, SimtShape<SIMT_DW>::kStN), jobs * E));
 }
 
 cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
