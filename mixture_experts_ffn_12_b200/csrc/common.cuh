@@ -42,6 +42,13 @@ __device__ __forceinline__ void pdl_enter() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The same in two parts, for kernels that set up barriers and TMEM in between: nothing that
+// an earlier kernel may have written is read before pdl_wait.
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Host: launch `kern` on `stream` with programmatic stream serialization allowed.
 // Errors are left for cudaGetLastError, as with <<<>>>.
 template <typename... KArgs, typename... Args>

@@ -97,7 +97,7 @@ struct Mx4Tile {
 template <typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     grouped_gemm_mx4_kernel(const __grid_constant__ Mx4Args args) {
-  pdl_enter();
+  pdl_launch_dependents();
   using LY = Mx4Layout;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -143,7 +143,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    mx4_group_table<kMx4Rows>(args.group_off, G, args.m_total, goff, tile_off);
     if (lane == 0) {
       tma_prefetch_desc(&args.w);
       tma_prefetch_desc(&args.x[0]);
@@ -155,6 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
+  pdl_wait();
+  if (warp == 0) group_table(args.group_off, G, args.m_total, kMx4Rows, goff, tile_off);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them

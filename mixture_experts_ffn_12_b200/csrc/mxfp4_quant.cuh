@@ -179,10 +179,9 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const T* __restrict
   }
 }
 
-// Row-group table of a kernel: goff[g] (clamped into [0, rows]) and the prefix of BM-row
-// blocks per group.  Called by one whole warp; G <= kMaxGroups.
-template <int BM = kBM>
-__device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int rows, int* goff, int* blk) {
+// Row-group table of a kernel: goff[g] (clamped into [0, rows]) and the prefix of the groups'
+// blocks of at most `most` rows.  Called by one whole warp; G <= kMaxGroups.
+__device__ __forceinline__ void group_table(const int32_t* off, int G, int rows, int most, int* goff, int* blk) {
   const int lane = threadIdx.x & 31;
   int bad = 0;
   for (int g = lane; g <= G; g += 32) {
@@ -199,7 +198,7 @@ __device__ __forceinline__ void mx4_group_table(const int32_t* off, int G, int r
     if (g < G) {
       const int n = goff[g + 1] - goff[g];
       if (n < 0) bad = 1;
-      cnt = n > 0 ? (n + BM - 1) / BM : 0;
+      cnt = n > 0 ? (n + most - 1) / most : 0;
     }
     int incl = cnt;
 #pragma unroll
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat1
   pdl_enter();
   __shared__ int goff[kMaxGroups + 2];
   __shared__ int tile_off[kMaxGroups + 2];
-  if (threadIdx.x < 32) mx4_group_table<kMx4Rows>(off, G, rows, goff, tile_off);
+  if (threadIdx.x < 32) group_table(off, G, rows, kMx4Rows, goff, tile_off);
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const int kc = mx4_chunks(K);

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
   __shared__ int goff[kTable], toff[kTable];
   const int G = args.num_groups;
   if (KIND != SIMT_DW) {
-    if (threadIdx.x < 32) mx4_group_table<kStM>(args.group_off, G, args.m_total, goff, toff);
+    if (threadIdx.x < 32) group_table(args.group_off, G, args.m_total, kStM, goff, toff);
     __syncthreads();
   }
 

@@ -126,6 +126,7 @@ struct TrainArgs {
   const int32_t* group_off;   // [G+1]
   int num_groups;
   int m_total;                // R
+  int tile_rows;              // most rows in a tile's N (not DW): TrainLayout::ROWS, or a half or quarter
   int k_dim;                  // K (DX: of one half)
   __nv_bfloat16* gu;          // GATEUP (written), DH: [R, 2, F]
   float limit, alpha, gate_lo;
@@ -293,7 +294,7 @@ __device__ __forceinline__ void store_rows64(uint8_t* stage, T* out, size_t ldo,
 template <int KIND, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     ffn_train_kernel(const __grid_constant__ TrainArgs<KIND> args) {
-  pdl_enter();
+  pdl_launch_dependents();
   using LY = TrainLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -341,7 +342,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    mx4_group_table<LY::ROWS>(args.group_off, G, args.m_total, goff, tile_off);
     if (lane < args.num_jobs) {
       tma_prefetch_desc(&args.job[lane].a.single);
       tma_prefetch_desc(KIND == TR_DW ? &args.job[lane].bw.single : &args.job[lane].b[0]);
@@ -353,6 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     for (int i = threadIdx.x - 64; i < LY::ONES / 4; i += 128) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
   }
+  pdl_wait();
+  if (warp == 0) group_table(args.group_off, G, args.m_total, KIND == TR_DW ? kTrBM : args.tile_rows, goff, tile_off);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them

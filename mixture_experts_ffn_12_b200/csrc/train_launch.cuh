@@ -142,9 +142,25 @@ static TrainArgs<KIND> train_args(const Launch& L, int64_t R, int E, int k_dim, 
   return a;
 }
 
-// Row tiles of at most `most` rows that R rows of E experts can take.
-static int64_t train_row_tiles(int64_t R, int E, int most) { return (R + most - 1) / most + E; }
 static int64_t train_col_tiles(int n) { return (n + kTrBM - 1) / kTrBM; }
+
+// Rows of a tile: the most the kernel takes, halved (to 64 at least) while even experts'
+// tiles would not fill half of the CTA pairs, so that the halves still run at once.
+// (Backward of 7 experts of 143 rows, D = 1440, F = 720, 74 pairs: DH, 24 full tiles,
+// 22.2 us, halved 17.2; DX, 48 full tiles, 15.4 us, halved -- more than a wave -- 20.1.)
+static int train_tile_rows(const Launch& L, int64_t R, int E, int n, int most) {
+  const int64_t avg = std::max<int64_t>(1, (R + E - 1) / E), experts = std::min<int64_t>(E, R);
+  while (most > 64 && 2 * experts * ((avg + most - 1) / most) * train_col_tiles(n) <= L.num_sms / 2) most /= 2;
+  return most;
+}
+
+// Launches a product with n output columns: tiles of at most `most` rows.
+template <int KIND>
+static cudaError_t launch_rows(const Launch& L, TrainArgs<KIND>& a, int64_t R, int E, int n) {
+  a.tile_rows = train_tile_rows(L, R, E, n, TrainLayout<KIND>::ROWS);
+  const int64_t row_tiles = (R + a.tile_rows - 1) / a.tile_rows + E;
+  return launch_train<KIND, __nv_bfloat16>(L, a, row_tiles * train_col_tiles(n));
+}
 
 // Rows [R, K] in bf16 as the N operand: boxes of 64 elements x 32, 64, .. rows.
 static cudaError_t make_row_maps(CUtensorMap* m, int count, const void* ptr, uint64_t K, uint64_t R) {
@@ -170,8 +186,7 @@ cudaError_t expert_train_bf16(const Launch& L, int64_t R, int D, int F, int E, c
     j.bias1 = static_cast<const __nv_bfloat16*>(w.b_up);
     j.m = F;
     a.gu = static_cast<__nv_bfloat16*>(gu);
-    if ((e = launch_train<TR_GATEUP, __nv_bfloat16>(L, a, train_row_tiles(R, E, 128) * train_col_tiles(F))) != cudaSuccess)
-      return e;
+    if ((e = launch_rows(L, a, R, E, F)) != cudaSuccess) return e;
   }
   TrainArgs<TR_DOWN> a = train_args<TR_DOWN>(L, R, E, F, off, act);
   TrainJob& j = a.job[0];
@@ -180,7 +195,7 @@ cudaError_t expert_train_bf16(const Launch& L, int64_t R, int D, int F, int E, c
   j.out = y_perm;
   j.bias0 = static_cast<const __nv_bfloat16*>(w.b_down);
   j.m = D;
-  return launch_train<TR_DOWN, __nv_bfloat16>(L, a, train_row_tiles(R, E, 256) * train_col_tiles(D));
+  return launch_rows(L, a, R, E, D);
 }
 
 static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
@@ -197,8 +212,7 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     j.out = dgu;
     j.m = F;
     a.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));   // read only
-    if ((e = launch_train<TR_DH, __nv_bfloat16>(L, a, train_row_tiles(R, E, 256) * train_col_tiles(F))) != cudaSuccess)
-      return e;
+    if ((e = launch_rows(L, a, R, E, F)) != cudaSuccess) return e;
   }
   if (dx != nullptr) {
     TrainArgs<TR_DX> a = train_args<TR_DX>(L, R, E, F, off, act);
@@ -209,8 +223,7 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
       if ((e = make_tmap_halves(&j.b[q], dgu, F, R, 32 * (q + 1))) != cudaSuccess) return e;
     j.out = dx;
     j.m = D;
-    if ((e = launch_train<TR_DX, __nv_bfloat16>(L, a, train_row_tiles(R, E, 256) * train_col_tiles(D))) != cudaSuccess)
-      return e;
+    if ((e = launch_rows(L, a, R, E, D)) != cudaSuccess) return e;
   }
   TrainArgs<TR_DW> a = train_args<TR_DW>(L, R, E, 0, off, act);
   a.num_jobs = 0;

@@ -35,6 +35,9 @@ CASES = [
     ([300], 496, 272, BF16, "swiglu", False),
     ([0, 700, 3], 512, 720, BF16, "swiglu", True),
     ([40, 0, 513, 90], 1440, 336, BF16, "silu", True),
+    # enough tiles that they keep their full height (128 and 256 rows)
+    ([600, 0, 1030], 1440, 2880, BF16, "swiglu", True),
+    ([530, 770], 2880, 1456, BF16, "silu", False),
     (EDGES, 48, 80, F32, "swiglu", True),
     ([1], 16, 16, F32, "silu", False),
     ([130, 0, 67], 272, 144, F32, "swiglu", False),
