@@ -188,6 +188,17 @@ def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _workspace(ws: Optional[torch.Tensor], n: int, device: torch.device) -> torch.Tensor:
+    """`ws` (checked) or a new workspace of n bytes."""
+    if ws is None:
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws
+
+
 def _launch(what: str, device: torch.device, *args) -> None:
     """Calls the library function `what` with torch's current stream of `device` behind args, that device
     current.  Tensors in args are checked ones (``_want``): their addresses are passed."""
@@ -570,11 +581,7 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] 
     L, dev = _lib.load(), x.device
     if y is None:
         y = torch.empty((R, N), dtype=torch.float32 if out_f32 else torch.bfloat16, device=dev)
-    if ws is None:
-        n = _size(L.moe_mxfp4_linear_workspace_size(G, R, N, K), "moe_mxfp4_linear_workspace_size")
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-    elif ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    ws = _workspace(ws, _size(L.moe_mxfp4_linear_workspace_size(G, R, N, K), "moe_mxfp4_linear_workspace_size"), dev)
     _launch("moe_mxfp4_linear", dev, G, R, N, K, x, group_off, w.codes, w.tiles, bias, 1 if out_f32 else 0, y, ws,
             ws.numel() * ws.element_size())
     return y
@@ -692,12 +699,8 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
             if t is not None:
                 _want(name, t, (E, n), gdt, dev)
     dx = torch.empty_like(x_perm) if need_dx else None
-    nws = _size(L.moe_expert_ffn_backward_workspace_size(ctypes.byref(cfg), T),
-                "moe_expert_ffn_backward_workspace_size")
-    if ws is None:
-        ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
-    elif ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    ws = _workspace(ws, _size(L.moe_expert_ffn_backward_workspace_size(ctypes.byref(cfg), T),
+                              "moe_expert_ffn_backward_workspace_size"), dev)
     wst, gst = weights.c_struct(), grads.c_struct()
     _launch("moe_expert_ffn_backward", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h,
             dy_perm, dx, ctypes.byref(gst), ws, ws.numel() * ws.element_size())

@@ -488,17 +488,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
         }
         if (!ok) break;
       }
+      // every copy has landed before the CTA may leave (after a wait that gave up: see the end)
+      for (int q = 0; leader && ok && q < LY::STAGES; ++q) {
+        if (rank == 0 && ((issued >> q) & 1u)) ok = mbar_wait(&full[q], (issued_par >> q) & 1u, abort_flag, kDrainLimitNs);
+        if (ok && ((tails >> q) & 1u)) ok = mbar_wait(&landed[q], (tail_par >> q) & 1u, abort_flag, kDrainLimitNs);
+      }
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
-        // the peer's barrier cannot be polled from here: give loads in flight time to land
-        for (int q = 0; q < 2000; ++q) __nanosleep(1000);
-      }
-      for (int q = 0; leader && q < LY::STAGES; ++q) {
-        if (rank == 0 && ((issued >> q) & 1u))
-          if (!mbar_wait(&full[q], (issued_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
-        if ((tails >> q) & 1u)
-          if (!mbar_wait(&landed[q], (tail_par >> q) & 1u, never_flag, kDrainLimitNs)) flag_error(DEVERR_TIMEOUT);
       }
     }
     __syncwarp();
@@ -780,6 +777,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // A role that gave up leaves copies in flight whose barrier nobody waits for any more: both
+  // CTAs stay until they have landed (the peer waits for this one at the cluster barrier).
+  if (threadIdx.x == 0 && *abort_flag)
+    for (int q = 0; q < 2000; ++q) __nanosleep(1000);
   cluster_sync_all();   // no CTA leaves while its peer may still signal it or read its memory
   if (warp == 1) {
     tc_fence_after();
