@@ -8,10 +8,11 @@
 // and a block that holds an infinity or a NaN gets scale byte 255 (the E8M0 NaN) and
 // zero codes, so that it reads back as NaN instead of as a wrong number.
 //
-// Bound by memory: 2 (bf16) or 4 (fp32) bytes read and 0.53 written an element.  Four lanes
-// share a block (8 elements each): every 16-byte load and 4-byte store of a warp is one run
-// (two lanes a block, 32 bytes a lane, were slower), the block maximum takes two shuffles;
-// bf16 maxima and scaling run on packed pairs.
+// Bound by memory: 2 (bf16) or 4 (fp32) bytes read and 0.53 written an element, close to
+// where its instructions bound it too, so both count: two lanes share a block (16 elements
+// each, about 5 instructions an element where 8 each took 9), and their 32 bytes are one
+// access where the address allows it (as two accesses of 16 bytes, 32 apart, they ran
+// slower than 8 elements a lane).  bf16 maxima and scaling run on packed pairs.
 //
 // Scale layouts.  "Rows": [rows, K/32], what the MXFP4 expert weights of the layer use.
 // "Tiles": what the 4-bit x 4-bit product reads: for 128 rows and 128 elements of K one
@@ -97,83 +98,111 @@ __device__ __forceinline__ void unpack8(const uint4* raw, float (&v)[8]) {
   }
 }
 
-// 8 elements of a block that four neighbouring lanes share, as loaded: 8 codes and the scale
-// byte.
+// 32 bytes at once where `kA32` (a 32-byte aligned address), else in two.
+template <bool kA32>
+__device__ __forceinline__ void load32(uint4 (&v)[2], const uint4* p) {
+  if constexpr (kA32) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z),
+                   "=r"(v[1].w)
+                 : "l"(p));
+  } else {
+    v[0] = p[0];
+    v[1] = p[1];
+  }
+}
+template <bool kA32>
+__device__ __forceinline__ void store32(uint4* p, const uint4 (&v)[2]) {
+  if constexpr (kA32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0].x), "r"(v[0].y),
+                 "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w)
+                 : "memory");
+  } else {
+    p[0] = v[0];
+    p[1] = v[1];
+  }
+}
+
+// 16 elements of a block that a lane and its neighbour (lane ^ 1) share, as loaded: 16 codes
+// and the scale byte.
 template <typename T>
-__device__ __forceinline__ uint32_t mx4_quantize8(const uint4* raw, uint32_t& scale) {
-  uint32_t m;
+__device__ __forceinline__ uint2 mx4_quantize16(const uint4* raw, uint32_t& scale) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(raw);
+  uint32_t m;                                 // the largest |x| as fp32 bits: |x| orders as its bits do
   if constexpr (sizeof(T) == 2) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(raw);   // |x| orders as its bits do
-    uint32_t m2 = __vmaxu2(__vmaxu2(r[0] & 0x7FFF7FFFu, r[1] & 0x7FFF7FFFu),
-                           __vmaxu2(r[2] & 0x7FFF7FFFu, r[3] & 0x7FFF7FFFu));
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m2 = __vmaxu2(m2, r[j] & 0x7FFF7FFFu);
     m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
-    m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
     m = max(m2 & 0xFFFFu, m2 >> 16) << 16;
   } else {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(raw);
     m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, r[j] & 0x7FFFFFFFu);
+    for (int j = 0; j < 16; ++j) m = max(m, r[j] & 0x7FFFFFFFu);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   }
-  if (m >= 0x7F800000u) {   // an infinity or a NaN in the block
+  if (m >= 0x7F800000u) {                     // an infinity or a NaN in the block
     scale = 255;
-    return 0;
+    return make_uint2(0, 0);
   }
   const int X = mx4_exponent(m);
   scale = static_cast<uint32_t>(X + 127);
-  float v[8];
-  if constexpr (sizeof(T) == 2) {
-    const uint16_t ib = static_cast<uint16_t>((127 - X) << 7);    // 2^-X, X in [-127, 126]
-    const __nv_bfloat162 inv = __halves2bfloat162(__ushort_as_bfloat16(ib), __ushort_as_bfloat16(ib));
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+  uint2 q;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // exact, or so small that it rounds to zero either way
-      const float2 f = __bfloat1622float2(__hmul2(h[j], inv));
-      v[2 * j] = f.x;
-      v[2 * j + 1] = f.y;
+  for (int w = 0; w < 2; ++w) {
+    float v[8];
+    if constexpr (sizeof(T) == 2) {
+      const uint16_t ib = static_cast<uint16_t>((127 - X) << 7);    // 2^-X, X in [-127, 126]
+      const __nv_bfloat162 inv = __halves2bfloat162(__ushort_as_bfloat16(ib), __ushort_as_bfloat16(ib));
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw + w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {   // exact, or so small that it rounds to zero either way
+        const float2 f = __bfloat1622float2(__hmul2(h[j], inv));
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    } else {
+      const float inv = exp2_int(-X);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[8 * w + j]) * inv;
     }
-  } else {
-    const float inv = exp2_int(-X);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = reinterpret_cast<const float*>(raw)[j] * inv;
+    (w == 0 ? q.x : q.y) = e2m1x8(v);
   }
-  return e2m1x8(v);
+  return q;
 }
 
 // x [nblk, 32] -> codes [nblk, 16 B], scales [nblk]: rows of any width are runs of blocks.
-// A thread loads kMx4Unroll pieces before it uses the first (one load at a time leaves 32 KB
-// a SM outstanding, too little for HBM).
-constexpr int kMx4Unroll = 4;
-template <typename T>
+// A thread loads kMx4Unroll pieces before it uses the first.
+constexpr int kMx4Unroll = 2;
+template <typename T, bool kA32>
 __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const T* __restrict__ x, int64_t nblk,
-                                                             uint32_t* __restrict__ codes,
+                                                             uint2* __restrict__ codes,
                                                              uint8_t* __restrict__ scales) {
   pdl_enter();
-  const int64_t total = nblk * 4;   // lanes; whole warps take part in the shuffles
+  const int64_t total = nblk * 2;   // lanes; whole warps take part in the shuffles
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * kMx4Unroll;
-  constexpr int kWords = sizeof(T) / 2;   // 16-byte words of 8 elements
+  constexpr int kWords = sizeof(T);   // 16-byte words of 16 elements
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * 256 * kMx4Unroll; base < total; base += step) {
     const uint4* src = reinterpret_cast<const uint4*>(x) + base * kWords;
-    uint32_t* dst = codes + base;
-    uint8_t* sdst = scales + (base >> 2);
+    uint2* dst = codes + base;
+    uint8_t* sdst = scales + (base >> 1);
     const int left = static_cast<int>(min(total - base, static_cast<int64_t>(256 * kMx4Unroll)));
-    uint4 raw[kMx4Unroll][kWords];
+    uint4 raw[kMx4Unroll][kWords / 2][2] = {};
 #pragma unroll
     for (int u = 0; u < kMx4Unroll; ++u) {
       const int i = u * 256 + threadIdx.x;
+      if (i < left)
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) raw[u][w] = i < left ? __ldcs(src + i * kWords + w) : make_uint4(0, 0, 0, 0);
+        for (int w = 0; w < kWords / 2; ++w) load32<kA32>(raw[u][w], src + i * kWords + 2 * w);
     }
 #pragma unroll
     for (int u = 0; u < kMx4Unroll; ++u) {
       const int i = u * 256 + threadIdx.x;
       uint32_t s;
-      const uint32_t q = mx4_quantize8<T>(raw[u], s);
+      const uint2 q = mx4_quantize16<T>(raw[u][0], s);
       if (i < left) {
         dst[i] = q;
-        if ((i & 3) == 0) sdst[i >> 2] = static_cast<uint8_t>(s);
+        if ((i & 1) == 0) sdst[i >> 1] = static_cast<uint8_t>(s);
       }
     }
   }
@@ -216,11 +245,12 @@ __device__ __forceinline__ void group_table(const int32_t* off, int G, int rows,
 // tiles, the row tiles counted group after group.  Rows outside every group are skipped.
 // A warp takes `spans` runs of kMx4QuantSpan elements of a row (blockIdx.y picks which): the
 // row's place in the tiles is looked up once, all loads of a run are in flight before the
-// first is used, and the scales of 128 elements (four blocks, 16 lanes) leave as one word.
+// first is used, and the scales of 128 elements (four blocks, 8 lanes) leave as one word.
 constexpr int kMx4QuantSpan = 1024;
+template <bool kA32>
 __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, int rows, int K,
                                                               const int32_t* __restrict__ off, int G, int max_tiles,
-                                                              int spans, uint32_t* __restrict__ codes,
+                                                              int spans, uint2* __restrict__ codes,
                                                               uint8_t* __restrict__ tiles) {
   pdl_enter();
   __shared__ int goff[kMaxGroups + 2];
@@ -232,17 +262,17 @@ __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat1
   const int k_first = blockIdx.y * spans * kMx4QuantSpan;
   const int k_end = min(k_first + spans * kMx4QuantSpan, kc * 128);
   const int step = gridDim.x * 8;
-  constexpr int IT = kMx4QuantSpan / 256;
+  constexpr int IT = kMx4QuantSpan / 512;
   for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += step) {
     const __nv_bfloat16* src = x + static_cast<size_t>(row) * K;
-    uint32_t* crow = codes + (static_cast<size_t>(row) * K >> 3);
+    uint2* crow = codes + (static_cast<size_t>(row) * K >> 4);
     uint8_t* dst = nullptr;
     for (int kb = k_first; kb < k_end; kb += kMx4QuantSpan) {
-      uint4 raw[IT];
+      uint4 raw[IT][2] = {};
 #pragma unroll
       for (int t = 0; t < IT; ++t) {
-        const int k = kb + 256 * t + lane * 8;
-        raw[t] = k < K ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0, 0, 0, 0);
+        const int k = kb + 512 * t + lane * 16;
+        if (k < K) load32<kA32>(raw[t], reinterpret_cast<const uint4*>(src + k));
       }
       if (kb == k_first) {
         int lo = 0, hi = G;   // goff[lo] <= row < goff[hi] where the row is in a group
@@ -263,16 +293,16 @@ __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat1
       }
 #pragma unroll
       for (int t = 0; t < IT; ++t) {
-        const int k = kb + 256 * t + lane * 8;
+        const int k = kb + 512 * t + lane * 16;
         uint32_t s;
-        const uint32_t q = mx4_quantize8<__nv_bfloat16>(&raw[t], s);
-        if (k < K) crow[k >> 3] = q;
+        const uint2 q = mx4_quantize16<__nv_bfloat16>(raw[t], s);
+        if (k < K) crow[k >> 4] = q;
         else s = 127;
-        // lanes 0, 4, 8, 12 of each half warp hold the scales of a chunk's four blocks
-        uint32_t w = s << (8 * ((lane >> 2) & 3));
+        // lanes 0, 2, 4, 6 of each eight hold the scales of a chunk's four blocks
+        uint32_t w = s << (8 * ((lane >> 1) & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
         w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        w |= __shfl_xor_sync(0xffffffffu, w, 8);
-        if (dst != nullptr && (lane & 15) == 0 && k < kc * 128)
+        if (dst != nullptr && (lane & 7) == 0 && k < kc * 128)
           *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(k >> 7) * 1024) = w;
       }
     }
@@ -307,35 +337,49 @@ __global__ void __launch_bounds__(256) mx4_scale_tiles_kernel(const uint8_t* __r
 }
 
 // codes [nblk, 16 B], scales [nblk] -> values; scale byte 255 gives NaN.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* __restrict__ codes,
+template <typename T, bool kA32>
+__global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint2* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t nblk,
                                                                T* __restrict__ out) {
   pdl_enter();
-  const int64_t total = nblk * 4;
+  const int64_t total = nblk * 2;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * kMx4Unroll;
+  constexpr int kWords = sizeof(T);   // 16-byte words of 16 elements
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * 256 * kMx4Unroll; base < total; base += step) {
-    const uint32_t* src = codes + base;
-    const uint8_t* ssrc = scales + (base >> 2);
-    T* dst = out + base * 8;
+    const uint2* src = codes + base;
+    const uint8_t* ssrc = scales + (base >> 1);
+    uint4* dst = reinterpret_cast<uint4*>(out) + base * kWords;
     const int left = static_cast<int>(min(total - base, static_cast<int64_t>(256 * kMx4Unroll)));
-    uint32_t q[kMx4Unroll];
+    uint2 q[kMx4Unroll];
     int s[kMx4Unroll];
 #pragma unroll
     for (int u = 0; u < kMx4Unroll; ++u) {
       const int i = u * 256 + threadIdx.x;
-      q[u] = i < left ? src[i] : 0;
-      s[u] = i < left ? ssrc[i >> 2] : 0;
+      q[u] = i < left ? src[i] : make_uint2(0, 0);
+      s[u] = i < left ? ssrc[i >> 1] : 0;
     }
 #pragma unroll
     for (int u = 0; u < kMx4Unroll; ++u) {
       const int i = u * 256 + threadIdx.x;
       const float f = s[u] == 255 ? __uint_as_float(0x7FC00000u) : exp2_int(s[u] - 127);
-      float v[8];
-      e2m1x8_to_f32(q[u], v);
+      float v[16];
+      e2m1x8_to_f32(q[u].x, *reinterpret_cast<float(*)[8]>(v));
+      e2m1x8_to_f32(q[u].y, *reinterpret_cast<float(*)[8]>(v + 8));
+      uint4 o[kWords / 2][2];
+      uint32_t* w = reinterpret_cast<uint32_t*>(o);
+      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= f;
-      if (i < left) store8<T>(dst + i * 8, v);
+        for (int j = 0; j < 8; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j] * f, v[2 * j + 1] * f);
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j] * f);
+      }
+      if (i < left)
+#pragma unroll
+        for (int p = 0; p < kWords / 2; ++p) store32<kA32>(dst + i * kWords + 2 * p, o[p]);
     }
   }
 }
@@ -344,30 +388,34 @@ static int mx4_blocks(const Launch& L, int64_t threads) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((threads + 255) / 256, int64_t(L.num_sms) * 8)));
 }
 
+static bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+template <typename T>
+static void launch_quant_rows(const Launch& L, int64_t nblk, const void* x, uint8_t* codes, uint8_t* scales) {
+  auto kern = aligned32(x) ? mx4_quant_rows_kernel<T, true> : mx4_quant_rows_kernel<T, false>;
+  pdl_launch(kern, dim3(mx4_blocks(L, nblk * 2 / kMx4Unroll + 1)), dim3(256), 0, L.stream, static_cast<const T*>(x),
+             nblk, reinterpret_cast<uint2*>(codes), scales);
+}
+
 cudaError_t mx4_quant_rows(const Launch& L, bool bf16, int64_t rows, int K, const void* x, uint8_t* codes,
                            uint8_t* scales) {
-  const int64_t nblk = rows * (K / 32);
-  const int blocks = mx4_blocks(L, nblk * 4 / kMx4Unroll + 1);
-  if (bf16)
-    pdl_launch(mx4_quant_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, L.stream,
-               static_cast<const __nv_bfloat16*>(x), nblk, reinterpret_cast<uint32_t*>(codes), scales);
-  else
-    pdl_launch(mx4_quant_rows_kernel<float>, dim3(blocks), dim3(256), 0, L.stream, static_cast<const float*>(x), nblk,
-               reinterpret_cast<uint32_t*>(codes), scales);
+  if (bf16) launch_quant_rows<__nv_bfloat16>(L, rows * (K / 32), x, codes, scales);
+  else launch_quant_rows<float>(L, rows * (K / 32), x, codes, scales);
   count_launch();
   return cudaGetLastError();
 }
 
+template <typename T>
+static void launch_dequant_rows(const Launch& L, int64_t nblk, const uint8_t* codes, const uint8_t* scales, void* out) {
+  auto kern = aligned32(out) ? mx4_dequant_rows_kernel<T, true> : mx4_dequant_rows_kernel<T, false>;
+  pdl_launch(kern, dim3(mx4_blocks(L, nblk * 2 / kMx4Unroll + 1)), dim3(256), 0, L.stream,
+             reinterpret_cast<const uint2*>(codes), scales, nblk, static_cast<T*>(out));
+}
+
 cudaError_t mx4_dequant_rows(const Launch& L, bool bf16, int64_t rows, int K, const uint8_t* codes,
                              const uint8_t* scales, void* out) {
-  const int64_t nblk = rows * (K / 32);
-  const int blocks = mx4_blocks(L, nblk * 4 / kMx4Unroll + 1);
-  if (bf16)
-    pdl_launch(mx4_dequant_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, L.stream,
-               reinterpret_cast<const uint32_t*>(codes), scales, nblk, static_cast<__nv_bfloat16*>(out));
-  else
-    pdl_launch(mx4_dequant_rows_kernel<float>, dim3(blocks), dim3(256), 0, L.stream,
-               reinterpret_cast<const uint32_t*>(codes), scales, nblk, static_cast<float*>(out));
+  if (bf16) launch_dequant_rows<__nv_bfloat16>(L, rows * (K / 32), codes, scales, out);
+  else launch_dequant_rows<float>(L, rows * (K / 32), codes, scales, out);
   count_launch();
   return cudaGetLastError();
 }
@@ -392,9 +440,10 @@ cudaError_t mx4_quant_tiles(const Launch& L, int64_t R, int K, const void* x, co
   const int runs = (K + kMx4QuantSpan - 1) / kMx4QuantSpan;
   const int spans = R >= int64_t(32) * L.num_sms ? runs : 1;
   const unsigned bx = static_cast<unsigned>(std::min<int64_t>((R + 7) / 8, int64_t(L.num_sms) * 8));
-  pdl_launch(mx4_quant_tiles_kernel, dim3(bx, (runs + spans - 1) / spans), dim3(256), 0, L.stream,
+  auto kern = aligned32(x) ? mx4_quant_tiles_kernel<true> : mx4_quant_tiles_kernel<false>;
+  pdl_launch(kern, dim3(bx, (runs + spans - 1) / spans), dim3(256), 0, L.stream,
              static_cast<const __nv_bfloat16*>(x), static_cast<int>(R), K, off, G,
-             static_cast<int>(mx4_row_tiles(R, G)), spans, reinterpret_cast<uint32_t*>(codes), tiles);
+             static_cast<int>(mx4_row_tiles(R, G)), spans, reinterpret_cast<uint2*>(codes), tiles);
   count_launch();
   return cudaGetLastError();
 }
