@@ -16,7 +16,8 @@
 // the mxf4 MMA reads 4-bit operands packed); the scales come as ready-made 512-byte chunks
 // (mxfp4_quant.cuh) by TMA, tcgen05.cp brings them to TMEM, four MMAs of K = 64.
 //
-// Roles (384 threads a CTA): warp 0 producer of the codes, warp 11 of the scales; warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue; warp 10 the tile
+// Roles (384 threads a CTA): warp 0 producer of the weights, warp 11 of the rows (weights are
+// on their way while the quantizer before this kernel still writes the rows); warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue; warp 10 the tile
 // scheduler.  Waits bounded and the closing cluster barrier as in grouped_gemm_pair.cuh.
 #pragma once
 
@@ -154,7 +155,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  pdl_wait();
+  // No wait for the quantizer here: it started after every earlier kernel was complete, so the
+  // offsets and the weights are in place; only the producer of the rows waits for it.
   if (warp == 0) group_table(args.group_off, G, args.m_total, kMx4Rows, goff, tile_off);
   tc_fence_before();
   __syncthreads();
@@ -223,10 +225,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     }
     __syncwarp();
   } else if (warp == 0) {
-    // ------------------------------------------------------------ producer of the codes (both CTAs)
+    // ------------------------------------------------------------ producer of the weights (both CTAs)
     {
       const bool leader = elect_one();
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      const int NBW = (args.n_out + 127) / 128;
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;
       Mx4Tile ti;
@@ -235,8 +238,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
         uniform(ti);
         if (ti.g < 0) break;
         const int q32 = (ti.n + 63) / 64;                  // boxes of 32 rows in half of the rows
-        const CUtensorMap* tx = &args.x[q32 - 1];
-        const int row = ti.r0 + rank * (ti.n / 2), col = ti.m0 + rank * 128;
+        const int col = ti.m0 + rank * 128;
+        // the pair's second block may lie behind the last one: its columns are not stored
+        const int wrow = (ti.g * NBW + min(ti.m0 / 128 + rank, NBW - 1)) * KB * (LY::SFA_BYTES / 256);
         const uint32_t bytes = 2u * (LY::A_BYTES + q32 * 32 * 128 + LY::SFA_BYTES + LY::SFB_BYTES);
         for (int kb = 0; kb < KB; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim))) { ok = false; break; }
@@ -245,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
           if (leader) {
             if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
             tma_load_3d_pair(st, &args.w, fb, kb * 128, col, ti.g);
-            tma_load_2d_pair(st + LY::A_BYTES, tx, fb, kb * 128, row);
+            tma_load_2d_pair(st + LY::A_BYTES + LY::B_BYTES, &args.sw, fb, 0, wrow + kb * (LY::SFA_BYTES / 256));
           }
           __syncwarp();
           issued |= 1u << s;
@@ -264,28 +268,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     }
     __syncwarp();
   } else if (warp == 11) {
-    // ------------------------------------------------------------ producer of the scales (both CTAs)
+    // ------------------------------------------------------------ producer of the rows (both CTAs)
     {
       const bool leader = elect_one();
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-      const int NBW = (args.n_out + 127) / 128;
       int s = 0;
       uint32_t ph = 0;
       Mx4Tile ti;
+      pdl_wait();   // the quantizer's codes and scales
       for (int n = 0;; ++n) {
         if (!next_tile(n, ti, true)) { ok = false; break; }
         uniform(ti);
         if (ti.g < 0) break;
-        // the pair's second block may lie behind the last one: its columns are not stored
-        const int wrow = (ti.g * NBW + min(ti.m0 / 128 + rank, NBW - 1)) * KB * (LY::SFA_BYTES / 256);
-        const int xrow = ti.xt * KB * (LY::SFB_BYTES / 256);
+        const CUtensorMap* tx = &args.x[(ti.n + 63) / 64 - 1];
+        const int row = ti.r0 + rank * (ti.n / 2), xrow = ti.xt * KB * (LY::SFB_BYTES / 256);
         for (int kb = 0; kb < KB; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort_flag, lim))) { ok = false; break; }
-          uint8_t* sf = smem + s * LY::STAGE_BYTES + LY::A_BYTES + LY::B_BYTES;
+          uint8_t* st = smem + s * LY::STAGE_BYTES + LY::A_BYTES;
           const uint32_t fb = full_leader + static_cast<uint32_t>(s) * 8u;
           if (leader) {
-            tma_load_2d_pair(sf, &args.sw, fb, 0, wrow + kb * (LY::SFA_BYTES / 256));
-            tma_load_2d_pair(sf + LY::SFA_BYTES, &args.sx, fb, 0, xrow + kb * (LY::SFB_BYTES / 256));
+            tma_load_2d_pair(st, tx, fb, kb * 128, row);
+            tma_load_2d_pair(st + LY::B_BYTES + LY::SFA_BYTES, &args.sx, fb, 0, xrow + kb * (LY::SFB_BYTES / 256));
           }
           __syncwarp();
           if (++s == kMx4Stages) { s = 0; ph ^= 1u; }

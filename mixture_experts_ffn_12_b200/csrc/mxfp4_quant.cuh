@@ -252,7 +252,10 @@ __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat1
                                                               const int32_t* __restrict__ off, int G, int max_tiles,
                                                               int spans, uint2* __restrict__ codes,
                                                               uint8_t* __restrict__ tiles) {
-  pdl_enter();
+  // First the wait, then the dependents: the product that follows starts when everything
+  // before this kernel is complete, and may read weights and offsets while this one runs.
+  pdl_wait();
+  pdl_launch_dependents();
   __shared__ int goff[kMaxGroups + 2];
   __shared__ int tile_off[kMaxGroups + 2];
   if (threadIdx.x < 32) group_table(off, G, rows, kMx4Rows, goff, tile_off);
