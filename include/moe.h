@@ -448,8 +448,10 @@ typedef struct {
  *   biases' column sums, overwritten (zero for an expert without rows).
  * bf16 layers: dg and du are rounded to bf16 before the products that read them
  * (tensor-core operands); every sum is fp32.  fp32 layers: fp32 FMA throughout.
- * The biases of `weights` are not read.  Deterministic.  T = 0 zeroes the
- * gradients.  ws: moe_expert_ffn_backward_workspace_size bytes. */
+ * The biases of `weights` are not read; their gradients are sums of dg and du as
+ * they are before that rounding.  Deterministic.  T = 0 zeroes the gradients.
+ * ws: moe_expert_ffn_backward_workspace_size bytes; on return it begins with
+ * (dg, du) [R, 2, F] in dtype, as rounded. */
 MOE_API size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T);
 MOE_API moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
                                              const int32_t* expert_off, const moe_expert_weights_t* weights,

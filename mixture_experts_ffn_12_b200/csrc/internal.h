@@ -154,11 +154,12 @@ cudaError_t expert_train_f32(const Launch& L, int64_t R, int D, int F, int E, co
 struct ExpertGrads {
   void *w_gate, *w_up, *w_down, *b_gate, *b_up, *b_down;   // each may be null
 };
-// dgu [R, 2, F] scratch in the layer dtype; dx may be null; gradients of the weights in the
+size_t expert_backward_bytes(bool bf16, int64_t R, int F, int E);
+// ws: expert_backward_bytes, beginning with dgu [R, 2, F] in the layer dtype; dx may be null; gradients of the weights in the
 // layer dtype, or fp32 if grad_f32.
 cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
                             const int32_t* expert_off, const ExpertWeights& w, const Activation& act, const void* gu,
-                            const void* h, const void* dy, void* dgu, void* dx, const ExpertGrads& grads,
+                            const void* h, const void* dy, void* ws, void* dx, const ExpertGrads& grads,
                             bool grad_f32);
 cudaError_t combine_backward(const Launch& L, bool bf16, int64_t T, int D, int k, const void* dy, const void* y_perm,
                              const int32_t* row_of_slot, const float* w, void* dy_perm, float* dw);

@@ -901,7 +901,8 @@ moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t 
 
 size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T) {
   if (check_train(cfg, MOE_ACT_SWIGLU) != MOE_OK || !check_T(T, cfg->num_experts_per_tok)) return size_t(-1);
-  return size_t(T) * cfg->num_experts_per_tok * 2 * cfg->intermediate_size * elem_size(cfg);
+  return moe::expert_backward_bytes(cfg->dtype == MOE_BF16, T * cfg->num_experts_per_tok, cfg->intermediate_size,
+                                    cfg->num_local_experts);
 }
 
 moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,

@@ -28,9 +28,13 @@
 // operands, before the MMA reads them (zeroing one would let an infinity or a NaN of a
 // neighbouring expert through as 0 * inf).
 //
-// Bias gradients: for the tiles of the first column block, which DW keeps 128 columns wide,
-// the issuer adds one N = 16 MMA a step whose B operand is a tile of ones, into TMEM columns
-// that the tile leaves free: the sums cost no further pass over dy and dgu.
+// Bias gradients.  db_down = column sums of dy: for the tiles of the first column block,
+// which that gradient keeps 128 columns wide, the issuer adds one N = 16 MMA a step whose B
+// operand is a tile of ones, into TMEM columns that the tile leaves free: no further pass
+// over dy.  db_gate and db_up are sums of dg and du before their rounding to bf16: DH's
+// epilogue lanes, each one column, add up their rows and leave the sums of a tile in the
+// workspace; DW adds an expert's tiles in order.  (Sums of the rounded values, by the same
+// ones, were off by up to twice as much where a sum cancels.)
 //
 // dg and du are rounded to bf16 between DH and the two products that read them (they are
 // tensor-core operands); all sums are fp32.
@@ -113,7 +117,8 @@ struct TrainJob {
     CUtensorMap b[4];   // the others
   };
   void* out;
-  void* bias_out;   // DW: [G, m] column sums of A, or null
+  void* bias_out;     // DW: [G, m] bias gradient, or null
+  const float* part;  // DW: its sums by row tile and epilogue half, part_ld apart; null: column sums of A
   const __nv_bfloat16 *bias0, *bias1;   // GATEUP (gate, up), DOWN: [G, m], or null
   int m, n;         // DW: rows and columns of the gradient;  else m = columns of the output
   int nt;           // DW: column blocks
@@ -126,9 +131,12 @@ struct TrainArgs {
   const int32_t* group_off;   // [G+1]
   int num_groups;
   int m_total;                // R
-  int tile_rows;              // most rows in a tile's N (not DW): TrainLayout::ROWS, or a half or quarter
+  int tile_rows;              // most rows in a tile's N: TrainLayout::ROWS, or a half or quarter (DW: DH's)
   int k_dim;                  // K (DX: of one half)
   __nv_bfloat16* gu;          // GATEUP (written), DH: [R, 2, F]
+  float* part;                // DH: [part_tiles][2 halves][2][F] sums of dg and du
+  int part_tiles;             // DH, DW (clamp for offsets that are not ascending)
+  int part_ld;                // 2 F
   float limit, alpha, gate_lo;
   unsigned long long wait_limit_ns;
 };
@@ -203,7 +211,8 @@ struct TrainTile {
   int n;                // MMA N
   int kb;               // 64-deep K blocks
   int r0, rows;         // DW: the expert's rows;  others: the tile's
-  int sums;             // DW: bias gradients wanted of this tile
+  int sums;             // DW: bias gradient wanted of this tile: 1 by the ones, 2 from the row tiles' sums
+  int rt;               // DH: row tile, counted over the experts
 };
 
 // DW: the last K block of the tile ends inside a 16-row MMA step.
@@ -237,7 +246,7 @@ __device__ __forceinline__ TrainTile train_tile(int i, const int* tile_off, cons
     t.r0 = goff[t.g];
     t.rows = max(0, goff[t.g + 1] - t.r0);
     t.kb = (t.rows + kTrBK - 1) / kTrBK;
-    t.sums = t.n0 == 0 && a.job[t.job].bias_out != nullptr ? 1 : 0;
+    t.sums = t.n0 != 0 || a.job[t.job].bias_out == nullptr ? 0 : a.job[t.job].part == nullptr ? 1 : 2;
   } else {
     // tiles of an expert: its row tiles fastest (they share the weight columns)
     const int mt = (a.job[0].m + kTrBM - 1) / kTrBM;
@@ -252,6 +261,7 @@ __device__ __forceinline__ TrainTile train_tile(int i, const int* tile_off, cons
     const int mb = i / rt, r = i - mb * rt;
     const int per = ((rows + rt - 1) / rt + 15) / 16 * 16;
     t.m0 = mb * kTrBM;
+    t.rt = tile_off[lo] + r;
     t.r0 = goff[lo] + r * per;
     t.rows = min(per, rows - r * per);
     t.n = (t.rows + 15) / 16 * 16;
@@ -354,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     fence_proxy_async_smem();
   }
   pdl_wait();
-  if (warp == 0) group_table(args.group_off, G, args.m_total, KIND == TR_DW ? kTrBM : args.tile_rows, goff, tile_off);
+  if (warp == 0) group_table(args.group_off, G, args.m_total, args.tile_rows, goff, tile_off);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them
@@ -521,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
         uniform(ti);
         if (ti.job < 0) break;
         const uint32_t idesc = make_idesc(kTrBM, ti.n, 1u) | (LY::A_KMAJOR ? 0u : 1u << 15) | (KIND == TR_DW ? 1u << 16 : 0u);
-        const bool sums = KIND == TR_DW && ti.sums != 0;
+        const bool sums = KIND == TR_DW && ti.sums == 1;
         const int acc = n & 1;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccStride);
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1u, abort_flag, lim))) { ok = false; break; }
@@ -606,11 +616,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
           store_rows64<OutT>(stage, out + c, jb.n, rows, width - c, v);
         }
         if (half == 0 && ti.sums) {
-          float b[8];
-          tmem_ld8(tbase + kTrOnesCol, b);
-          tmem_ld_wait();
+          float sum = 0.0f;
+          if (ti.sums == 1) {
+            float b[8];
+            tmem_ld8(tbase + kTrOnesCol, b);
+            tmem_ld_wait();
+            sum = none ? 0.0f : b[0];
+          } else if (lane < rows) {
+            const int last = min(tile_off[ti.g + 1], args.part_tiles);
+            for (int t = 2 * tile_off[ti.g]; t < 2 * last; ++t) sum += jb.part[static_cast<size_t>(t) * args.part_ld + row0 + lane];
+          }
           if (lane < rows) {
-            const float sum = none ? 0.0f : b[0];
             OutT* bo = static_cast<OutT*>(jb.bias_out) + row_base + row0 + lane;
             if constexpr (sizeof(OutT) == 2) *bo = __float2bfloat16_rn(sum);
             else *bo = sum;
@@ -638,6 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
           if (cvalid && jb.bias0 != nullptr) bias0 = __bfloat162float(jb.bias0[bi]);
           if (KIND == TR_GATEUP && cvalid && jb.bias1 != nullptr) bias1 = __bfloat162float(jb.bias1[bi]);
         }
+        float sum_g = 0.0f, sum_u = 0.0f;   // DH: of this lane's column
         uint32_t pg[8], pu[8];
         auto fetch = [&](int c) {
           if constexpr (KIND == TR_DH) {
@@ -695,6 +712,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
               float dg0, du0, dg1, du1;
               act_grad(v[2 * j], g.x, u.x, args.limit, args.alpha, args.gate_lo, dg0, du0);
               act_grad(v[2 * j + 1], g.y, u.y, args.limit, args.alpha, args.gate_lo, dg1, du1);
+              if (c + 2 * j < ti.rows) {   // accumulator columns past the tile's rows hold other rows' products
+                sum_g += dg0;
+                sum_u += du0;
+              }
+              if (c + 2 * j + 1 < ti.rows) {
+                sum_g += dg1;
+                sum_u += du1;
+              }
               dgs[j] = trade_pair(dg0, dg1);
               dus[j] = trade_pair(du0, du1);
             }
@@ -715,6 +740,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
               if (c + j < rows) *reinterpret_cast<uint32_t*>(o) = both;
             }
           }
+        }
+        if (KIND == TR_DH && args.part != nullptr && cvalid && ti.rt < args.part_tiles) {
+          float* p = args.part + static_cast<size_t>(2 * ti.rt + half) * args.part_ld + col;
+          p[0] = sum_g;
+          p[M] = sum_u;
         }
       }
       tc_fence_before();

@@ -154,6 +154,23 @@ static int train_tile_rows(const Launch& L, int64_t R, int E, int n, int most) {
   return most;
 }
 
+// Workspace of the backward pass: dgu [R, 2, F], then (bf16) the sums of dg and du by row tile
+// (of 64 rows at least) and epilogue half.
+struct BackwardLayout {
+  size_t part, total;
+};
+static BackwardLayout backward_layout(bool bf16, int64_t R, int F, int E) {
+  BackwardLayout l{};
+  l.part = static_cast<size_t>(R) * 2 * F * (bf16 ? 2 : 4);
+  l.total = l.part;
+  if (bf16) {
+    l.part = (l.part + 255) / 256 * 256;
+    l.total = l.part + static_cast<size_t>((R + 63) / 64 + E) * 2 * 2 * F * 4;
+  }
+  return l;
+}
+size_t expert_backward_bytes(bool bf16, int64_t R, int F, int E) { return backward_layout(bf16, R, F, E).total; }
+
 // Launches a product with n output columns: tiles of at most `most` rows.
 template <int KIND>
 static cudaError_t launch_rows(const Launch& L, TrainArgs<KIND>& a, int64_t R, int E, int n) {
@@ -200,9 +217,15 @@ cudaError_t expert_train_bf16(const Launch& L, int64_t R, int D, int F, int E, c
 
 static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F, int E, const void* x_perm,
                                         const int32_t* off, const ExpertWeights& w, const Activation& act,
-                                        const void* gu, const void* h, const void* dy, void* dgu, void* dx,
+                                        const void* gu, const void* h, const void* dy, void* ws, void* dx,
                                         const ExpertGrads& gr, bool grad_f32) {
   cudaError_t e;
+  const BackwardLayout LY = backward_layout(true, R, F, E);
+  void* dgu = ws;
+  float* part = (gr.b_gate != nullptr || gr.b_up != nullptr) ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + LY.part)
+                                                             : nullptr;
+  const int dh_rows = train_tile_rows(L, R, E, F, TrainLayout<TR_DH>::ROWS);
+  const int part_tiles = static_cast<int>((R + dh_rows - 1) / dh_rows + E);
   __nv_bfloat16* dg = static_cast<__nv_bfloat16*>(dgu);
   if (dx != nullptr || gr.w_gate != nullptr || gr.w_up != nullptr) {
     TrainArgs<TR_DH> a = train_args<TR_DH>(L, R, E, D, off, act);
@@ -212,6 +235,9 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     j.out = dgu;
     j.m = F;
     a.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));   // read only
+    a.part = part;
+    a.part_tiles = part_tiles;
+    a.part_ld = 2 * F;
     if ((e = launch_rows(L, a, R, E, F)) != cudaSuccess) return e;
   }
   if (dx != nullptr) {
@@ -227,22 +253,26 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   }
   TrainArgs<TR_DW> a = train_args<TR_DW>(L, R, E, 0, off, act);
   a.num_jobs = 0;
+  a.tile_rows = dh_rows;
+  a.part_tiles = part_tiles;
+  a.part_ld = 2 * F;
   int64_t tiles = 0;
-  auto add = [&](void* out, void* bias_out, const void* pa, int m, int64_t lda, const void* pb, int n) {
+  auto add = [&](void* out, void* bias_out, const float* sums, const void* pa, int m, int64_t lda, const void* pb, int n) {
     if (out == nullptr) return cudaSuccess;
     TrainJob& j = a.job[a.num_jobs++];
     j.out = out;
     j.bias_out = bias_out;
+    j.part = bias_out == nullptr ? nullptr : sums;
     j.m = m;
     j.n = n;
-    j.nt = train_col_blocks(n, bias_out != nullptr);
+    j.nt = train_col_blocks(n, bias_out != nullptr && sums == nullptr);
     tiles += int64_t(E) * (train_col_tiles(m)) * j.nt;
     const cudaError_t r = make_mn_maps(&j.a, pa, m, R, lda, 0);
     return r != cudaSuccess ? r : make_mn_maps(&j.bw, pb, n, R, n, 0);
   };
-  if ((e = add(gr.w_down, gr.b_down, dy, D, D, h, F)) != cudaSuccess) return e;
-  if ((e = add(gr.w_gate, gr.b_gate, dg, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
-  if ((e = add(gr.w_up, gr.b_up, dg + F, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
+  if ((e = add(gr.w_down, gr.b_down, nullptr, dy, D, D, h, F)) != cudaSuccess) return e;
+  if ((e = add(gr.w_gate, gr.b_gate, part, dg, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
+  if ((e = add(gr.w_up, gr.b_up, part == nullptr ? nullptr : part + F, dg + F, F, 2 * F, x_perm, D)) != cudaSuccess) return e;
   if (a.num_jobs == 0) return cudaSuccess;
   return grad_f32 ? launch_train<TR_DW, float>(L, a, tiles) : launch_train<TR_DW, __nv_bfloat16>(L, a, tiles);
 }
@@ -321,13 +351,13 @@ static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F,
 
 cudaError_t expert_backward(const Launch& L, bool bf16, int64_t R, int D, int F, int E, const void* x_perm,
                             const int32_t* expert_off, const ExpertWeights& w, const Activation& act, const void* gu,
-                            const void* h, const void* dy, void* dgu, void* dx, const ExpertGrads& grads,
+                            const void* h, const void* dy, void* ws, void* dx, const ExpertGrads& grads,
                             bool grad_f32) {
   if (bf16)
-    return expert_backward_bf16(L, R, D, F, E, x_perm, expert_off, w, act, gu, h, dy, dgu, dx, grads, grad_f32);
+    return expert_backward_bf16(L, R, D, F, E, x_perm, expert_off, w, act, gu, h, dy, ws, dx, grads, grad_f32);
   return expert_backward_f32(L, R, D, F, E, static_cast<const float*>(x_perm), expert_off, w, act,
                              static_cast<const float*>(gu), static_cast<const float*>(h),
-                             static_cast<const float*>(dy), static_cast<float*>(dgu), static_cast<float*>(dx), grads);
+                             static_cast<const float*>(dy), static_cast<float*>(ws), static_cast<float*>(dx), grads);
 }
 
 template <typename T, int KM>

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from train_util import HALF, Block, sum_bound, values, within  # noqa: E402
+from train_util import HALF, Block, backward_ws, sum_bound, values, within  # noqa: E402
 
 BF16, F32 = torch.bfloat16, torch.float32
 
@@ -103,7 +103,7 @@ def test_forward(api, counts, D, F, dtype, act, bias):
 def test_backward(api, counts, D, F, dtype, act, bias, grad_f32):
     b = Block(counts, D, F, dtype, bias, seed=1)
     cfg, gu, h, _ = _forward(api, b, act)
-    ws = torch.empty((b.R, 2, F), dtype=dtype, device="cuda")
+    ws, dgu_t = backward_ws(cfg, b)
     dx, gr = api.expert_ffn_backward(cfg, b.x, b.off_gpu, b.weights(api), gu, h, b.dy, act=act, grad_f32=grad_f32, ws=ws)
     torch.cuda.synchronize()
     assert api.last_device_error() == 0
@@ -114,7 +114,7 @@ def test_backward(api, counts, D, F, dtype, act, bias, grad_f32):
     dh = O.rows_times(dy, np.swapaxes(wd, 1, 2), b.off)
     dh_err = sum_bound(D, O.rows_times(np.abs(dy), np.abs(np.swapaxes(wd, 1, 2)), b.off))
     eg, eu = _act_bounds(dh_err, dh, guv[:, 0], guv[:, 1], act)
-    dgu = values(ws)
+    dgu = values(dgu_t)
     within("dg", dgu[:, 0], ref["dg"], eg + half * (np.abs(ref["dg"]) + eg) + 1e-38)
     within("du", dgu[:, 1], ref["du"], eu + half * (np.abs(ref["du"]) + eu) + 1e-38)
     dg, du = dgu[:, 0], dgu[:, 1]
@@ -130,13 +130,14 @@ def test_backward(api, counts, D, F, dtype, act, bias, grad_f32):
         got = getattr(gr, name)
         assert got.dtype == (F32 if grad_f32 else dtype)
         within(name, values(got), want, err + ghalf * (np.abs(want) + err))
-    for name, a in (("b_gate", dg), ("b_up", du), ("b_down", dy)):
+    # db_gate and db_up: sums of dg and du before their rounding, so against the oracle's own
+    for name, a, more in (("b_gate", ref["dg"], eg), ("b_up", ref["du"], eu), ("b_down", dy, 0.0 * dy)):
         got = getattr(gr, name)
         if not bias:
             assert got is None
             continue
         want = O.column_sums(a, b.off)
-        err = sum_bound(most, O.column_sums(np.abs(a), b.off))
+        err = sum_bound(most, O.column_sums(np.abs(a) + more, b.off)) + O.column_sums(more, b.off)
         within(name, values(got), want, err + ghalf * (np.abs(want) + err))
 
 
@@ -187,11 +188,12 @@ def test_rows_of_no_expert_are_left(api):
     _, want = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy)
     more = 9
     nan = lambda t: torch.cat([t, torch.full((more, *t.shape[1:]), float("nan"), dtype=t.dtype, device="cuda")])  # noqa: E731
-    ws = torch.full((b.R + more, 2, 48), 3.0, dtype=BF16, device="cuda")
+    ws, dgu = backward_ws(cfg, b, more)
+    dgu.fill_(3.0)
     _, got = api.expert_ffn_backward(cfg, nan(b.x), b.off_gpu, w, nan(gu), nan(h), nan(b.dy), ws=ws)
     torch.cuda.synchronize()
     assert api.last_device_error() == 0
-    assert (ws[b.R:] == 3.0).all()
+    assert (dgu[b.R:] == 3.0).all()
     for n in ("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down"):
         assert torch.equal(getattr(got, n), getattr(want, n))
 

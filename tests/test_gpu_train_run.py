@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from train_util import HALF, Block, sum_bound, values, within  # noqa: E402
+from train_util import HALF, Block, backward_ws, sum_bound, values, within  # noqa: E402
 
 BF16, F32 = torch.bfloat16, torch.float32
 
@@ -206,7 +206,7 @@ def test_one_gradient_through_the_abi(api):
         _, want = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy)
         out = torch.zeros_like(want.w_down)
         g = _lib.MoeExpertGrads(None, None, out.data_ptr(), None, None, None, 1 if dtype == F32 else 0)
-        ws = torch.empty(b.R * 2 * b.F * b.x.element_size(), dtype=torch.uint8, device="cuda")
+        ws, _ = backward_ws(cfg, b)
         p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
         before = _lib.load().moe_launch_count()
         assert _lib.load().moe_expert_ffn_backward(

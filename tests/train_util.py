@@ -2,8 +2,6 @@
 import numpy as np
 import torch
 
-import workloads as W
-
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}   # half a step, relative to the value
 
 
@@ -58,5 +56,10 @@ class Block:
         return api.ExpertWeights(self.wg, self.wu, self.wd, self.bg, self.bu, self.bd)
 
 
-def bf16_values(a):
-    return W.bf16_bits_to_f32(W.f32_to_bf16_bits(np.asarray(a, np.float32))).astype(np.float64)
+def backward_ws(cfg, b, extra_rows=0):
+    """(workspace of a backward call on the block's rows and extra_rows more, its (dg, du) [rows, 2, F])."""
+    import ctypes
+    from mixture_experts_ffn_12_b200 import _lib
+    R = b.R + extra_rows
+    ws = torch.empty(_lib.load().moe_expert_ffn_backward_workspace_size(ctypes.byref(cfg), R), dtype=torch.uint8, device="cuda")
+    return ws, ws[:R * 2 * b.F * b.x.element_size()].view(b.dtype).view(R, 2, b.F)
