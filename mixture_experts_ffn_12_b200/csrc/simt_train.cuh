@@ -38,6 +38,7 @@ struct SimtTrainArgs {
   int num_groups, m_total;
   const float* gu;            // DH
   float* gu_out;              // GATEUP
+  int early;                  // DW: behind a DX launch, starts beside it (as in train_gemm.cuh)
   float limit, alpha, gate_lo;
 };
 
@@ -67,7 +68,9 @@ __device__ __forceinline__ void cp_async16(float* dst, const float* src, bool va
 
 template <int KIND>
 __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainArgs args) {
-  pdl_enter();
+  if constexpr (KIND != SIMT_DX) pdl_launch_dependents();
+  if (KIND != SIMT_DW || !args.early) pdl_wait();
+  if constexpr (KIND == SIMT_DX) pdl_launch_dependents();
   using S = SimtShape<KIND>;
   constexpr int kStM = S::kStM, kStN = S::kStN, kStK = S::kStK, kStGroups = S::kStGroups;
   extern __shared__ __align__(16) float ring[];
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
       }
     }
   }
+  if (KIND == SIMT_DW && args.early) pdl_wait();
 }
 
 }  // namespace moe

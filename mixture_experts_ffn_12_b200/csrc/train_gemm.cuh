@@ -36,6 +36,11 @@
 // workspace; DW adds an expert's tiles in order.  (Sums of the rounded values, by the same
 // ones, were off by up to twice as much where a sum cancels.)
 //
+// DW needs nothing of DX, whose last wave of tiles leaves CTA pairs idle.  So DX lets its
+// dependents go only once its own wait is over: what DH wrote is then complete, DW starts on
+// the pairs that DX has left, and waits for DX at its end instead, so that the call's last
+// kernel ends last.
+//
 // dg and du are rounded to bf16 between DH and the two products that read them (they are
 // tensor-core operands); all sums are fp32.
 //
@@ -131,6 +136,7 @@ struct TrainArgs {
   const int32_t* group_off;   // [G+1]
   int num_groups;
   int m_total;                // R
+  int early;                  // DW: behind a DX launch, starts beside it
   int tile_rows;              // most rows in a tile's N: TrainLayout::ROWS, or a half or quarter (DW: DH's)
   int k_dim;                  // K (DX: of one half)
   __nv_bfloat16* gu;          // GATEUP (written), DH: [R, 2, F]
@@ -304,7 +310,7 @@ __device__ __forceinline__ void store_rows64(uint8_t* stage, T* out, size_t ldo,
 template <int KIND, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     ffn_train_kernel(const __grid_constant__ TrainArgs<KIND> args) {
-  pdl_launch_dependents();
+  if constexpr (KIND != TR_DX) pdl_launch_dependents();
   using LY = TrainLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -363,7 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     for (int i = threadIdx.x - 64; i < LY::ONES / 4; i += 128) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
   }
-  pdl_wait();
+  if (KIND != TR_DW || !args.early) pdl_wait();
+  if constexpr (KIND == TR_DX) pdl_launch_dependents();
   if (warp == 0) group_table(args.group_off, G, args.m_total, args.tile_rows, goff, tile_off);
   tc_fence_before();
   __syncthreads();
@@ -624,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
             sum = none ? 0.0f : b[0];
           } else if (lane < rows) {
             const int last = min(tile_off[ti.g + 1], args.part_tiles);
-            for (int t = 2 * tile_off[ti.g]; t < 2 * last; ++t) sum += jb.part[static_cast<size_t>(t) * args.part_ld + row0 + lane];
+            for (int t = 2 * tile_off[ti.g]; t < 2 * last; ++t) sum += __ldcg(jb.part + static_cast<size_t>(t) * args.part_ld + row0 + lane);
           }
           if (lane < rows) {
             OutT* bo = static_cast<OutT*>(jb.bias_out) + row_base + row0 + lane;
@@ -811,6 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
   // CTAs stay until they have landed (the peer waits for this one at the cluster barrier).
   if (threadIdx.x == 0 && *abort_flag)
     for (int q = 0; q < 2000; ++q) __nanosleep(1000);
+  if (KIND == TR_DW && args.early) pdl_wait();
   cluster_sync_all();   // no CTA leaves while its peer may still signal it or read its memory
   if (warp == 1) {
     tc_fence_after();

@@ -253,6 +253,7 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   }
   TrainArgs<TR_DW> a = train_args<TR_DW>(L, R, E, 0, off, act);
   a.num_jobs = 0;
+  a.early = dx != nullptr;
   a.tile_rows = dh_rows;
   a.part_tiles = part_tiles;
   a.part_ld = 2 * F;
@@ -334,6 +335,7 @@ static cudaError_t expert_backward_f32(const Launch& L, int64_t R, int D, int F,
     a.job[0] = SimtJob{dgu, f(w.w_gate), f(w.w_up), nullptr, nullptr, dx, nullptr, 2 * F, D, 0, D, F};
     if ((e = launch_simt<SIMT_DX>(L, a, dim3(row_tiles, simt_blocks(D, SimtShape<SIMT_DX>::kStN)))) != cudaSuccess) return e;
   }
+  a.early = dx != nullptr;
   int jobs = 0, most_m = 0, most_n = 0;
   auto add = [&](void* out, void* bias_out, const float* pa, int m, int lda, const float* pb, int n) {
     if (out == nullptr) return;
