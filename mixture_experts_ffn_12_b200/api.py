@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import Dict, Optional, Tuple
 
 import numpy as np
@@ -188,10 +189,15 @@ def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _rows_of(rows: int, n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """A new [rows, n] tensor (torch.empty takes 0.8 us longer to read its arguments)."""
+    return torch.empty_strided((rows, n), (n, 1), dtype=dtype, device=device)
+
+
 def _workspace(ws: Optional[torch.Tensor], n: int, device: torch.device) -> torch.Tensor:
     """`ws` (checked) or a new workspace of n bytes."""
     if ws is None:
-        return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+        return torch.empty_strided((max(n, 16),), (1,), dtype=torch.uint8, device=device)
     if ws.device != device:
         raise ValueError(f"ws is on {ws.device}, expected {device}")
     if not ws.is_contiguous():
@@ -500,8 +506,8 @@ def quantize_mxfp4(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     if K == 0 or K % 32:
         raise ValueError(f"quantize_mxfp4: the last dimension ({K}) must be a positive multiple of 32")
     lead = x.shape[:-1]
-    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
+    codes = x.new_empty((*lead, K // 2), dtype=torch.uint8)
+    scales = x.new_empty((*lead, K // 32), dtype=torch.uint8)
     _launch("moe_quantize_mxfp4", x.device, x.numel() // K, K, _DT_OF[x.dtype], x, codes, scales)
     return codes, scales
 
@@ -518,7 +524,7 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
     if K == 0 or K % 32:
         raise ValueError(f"dequantize_mxfp4: K = {K} must be a positive multiple of 32")
     _want("scales", scales, (*codes.shape[:-1], K // 32), torch.uint8, codes.device)
-    out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
+    out = codes.new_empty((*codes.shape[:-1], K), dtype=dtype)
     _launch("moe_dequantize_mxfp4", codes.device, out.numel() // K, K, codes, scales, _DT_OF[dtype], out)
     return out
 
@@ -580,7 +586,7 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] 
     G, N, K = _mxfp4_sizes(w.codes)
     L, dev = _lib.load(), x.device
     if y is None:
-        y = torch.empty((R, N), dtype=torch.float32 if out_f32 else torch.bfloat16, device=dev)
+        y = _rows_of(R, N, torch.float32 if out_f32 else torch.bfloat16, dev)
     ws = _workspace(ws, _size(L.moe_mxfp4_linear_workspace_size(G, R, N, K), "moe_mxfp4_linear_workspace_size"), dev)
     _launch("moe_mxfp4_linear", dev, G, R, N, K, x, group_off, w.codes, w.tiles, bias, 1 if out_f32 else 0, y, ws,
             ws.numel() * ws.element_size())
@@ -647,9 +653,10 @@ def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Ten
     code = _act_code(act)
     T = check_ffn_train_args(cfg, x_perm, expert_off, weights)
     R, dev, dt = x_perm.shape[0], x_perm.device, x_perm.dtype
-    gu = torch.empty((R, 2, cfg.intermediate_size), dtype=dt, device=dev)
-    h = torch.empty((R, cfg.intermediate_size), dtype=dt, device=dev)
-    y = torch.empty((R, cfg.hidden_size), dtype=dt, device=dev)
+    F = cfg.intermediate_size
+    gu = torch.empty_strided((R, 2, F), (2 * F, F, 1), dtype=dt, device=dev)
+    h = _rows_of(R, F, dt, dev)
+    y = torch.empty_like(x_perm)
     wst = weights.c_struct()
     _launch("moe_expert_ffn_train", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h, y)
     return gu, h, y
@@ -685,11 +692,10 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
     L, dev = _lib.load(), x_perm.device
     D, F, E = cfg.hidden_size, cfg.intermediate_size, cfg.num_local_experts
     gdt = torch.float32 if grad_f32 else torch_dtype(cfg)
-    has_bias = [b is not None for b in (weights.b_gate, weights.b_up, weights.b_down)]
     if grads is None:
-        new = lambda *s: torch.empty(s, dtype=gdt, device=dev)  # noqa: E731
-        grads = ExpertGrads(new(E, F, D), new(E, F, D), new(E, D, F), new(E, F) if has_bias[0] else None,
-                            new(E, F) if has_bias[1] else None, new(E, D) if has_bias[2] else None)
+        like = torch.empty_like if gdt == x_perm.dtype else functools.partial(torch.empty_like, dtype=gdt)
+        grads = ExpertGrads(*(None if p is None else like(p) for p in (
+            weights.w_gate, weights.w_up, weights.w_down, weights.b_gate, weights.b_up, weights.b_down)))
     else:
         for name, t, shape in (("grads.w_gate", grads.w_gate, (E, F, D)), ("grads.w_up", grads.w_up, (E, F, D)),
                                ("grads.w_down", grads.w_down, (E, D, F))):

@@ -3,17 +3,25 @@
 // train_gemm.cuh as one tiled kernel.
 //
 // These layers are small, so a launch is a chain of K steps more than a rate.  Tiles of 32
-// rows (an expert often has fewer) x 64 columns (32 for the products with the longest K and
-// the fewest columns), 4 x 4 outputs a thread, a three-deep ring of cp.async copies of 32
-// (64) K elements, so that no step waits for the load it has just issued, and four (eight)
-// groups of threads that each take a part of a step's K and add up at the end in a fixed
-// order: one group alone leaves a scheduler one warp, which issues every third cycle
-// (gate/up of 128 rows, D = 256, F = 512: 27 us; with four groups 18 us).  The weight
-// gradients, whose K is an expert's few rows, are the other way about: few steps and many
-// outputs, one group and tiles of 64 x 128 (32 x 64 with four groups: 3072 CTAs of one
-// step each, 25 us).  An operand tile is kept in the order in which it lies in memory,
-// [row][K] (16-byte pieces along K) or [K][row] (along the rows), with 16 bytes of padding a
-// row; either way a thread takes 4 x 4 of it per four K steps with four 16-byte loads.
+// rows (an expert often has fewer) x 32 columns, 4 x 4 outputs a thread, a three-deep ring of
+// cp.async copies of 64 K elements, so that no step waits for the load it has just issued,
+// and eight groups of threads that each take a part of a step's K and add up at the end in a
+// fixed order: one group alone leaves a scheduler one warp, which issues every third cycle.
+// Measured, forward + backward of 128 rows, 8 experts, D = 256, F = 512 (GPU time a pass, in
+// a graph): 18.4 + 33.7 us; gate/up and dH on 64 columns and 32 K elements 22.4 + 33.8 us, and
+// 129 + 202 against 128 + 199 us at 1024 rows, 4 experts, D = F = 640 (20 TFLOP/s: larger
+// tiles would serve such layers better, which the small ones would pay for).
+// The weight gradients, whose K is an expert's few rows, are the other way about: few steps
+// and many outputs, one group and tiles of 64 x 128 (32 x 64 with four groups: 3072 CTAs of
+// one step each, 25 against 13 us).  An operand tile is kept in the order in which it lies in
+// memory, [row][K] (16-byte pieces along K) or [K][row] (along the rows), with 16 bytes of
+// padding a row; either way a thread takes 4 x 4 of it per four K steps with four 16-byte loads.
+//
+// No kernel but DX lets its dependents start before it ends: several of these CTAs fit on
+// one SM, and a grid launched while another still fills most SMs crowds onto those that come
+// free first and runs there two deep (backward of the layer above, passes one after another:
+// 46.8 us with early starts throughout, 33.8 without).  DX lets DW start beside it, on the
+// half of the SMs that it leaves idle.
 #pragma once
 
 #include "train_gemm.cuh"
@@ -44,10 +52,9 @@ struct SimtTrainArgs {
 
 template <int KIND>
 struct SimtShape {
-  static constexpr bool kLongK = KIND == SIMT_DOWN || KIND == SIMT_DX;
   static constexpr int kStM = KIND == SIMT_DW ? 64 : 32;                     // rows of a tile
-  static constexpr int kStN = KIND == SIMT_DW ? 128 : kLongK ? 32 : 64;      // columns
-  static constexpr int kStK = kLongK ? 64 : 32;                              // K of a step
+  static constexpr int kStN = KIND == SIMT_DW ? 128 : 32;                    // columns
+  static constexpr int kStK = KIND == SIMT_DW ? 32 : 64;                     // K of a step
   static constexpr int kTX = kStN / 4, kPer = kTX * (kStM / 4), kStGroups = kStThreads / kPer;
   static constexpr bool kAK = KIND != SIMT_DW;                             // A tile [row][K]
   static constexpr bool kBK = KIND == SIMT_GATEUP || KIND == SIMT_DOWN;    // B tile [column][K]
@@ -68,7 +75,6 @@ __device__ __forceinline__ void cp_async16(float* dst, const float* src, bool va
 
 template <int KIND>
 __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainArgs args) {
-  if constexpr (KIND != SIMT_DX) pdl_launch_dependents();
   if (KIND != SIMT_DW || !args.early) pdl_wait();
   if constexpr (KIND == SIMT_DX) pdl_launch_dependents();
   using S = SimtShape<KIND>;
