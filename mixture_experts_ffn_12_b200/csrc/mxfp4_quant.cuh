@@ -13,6 +13,9 @@
 // each, about 5 instructions an element where 8 each took 9), and their 32 bytes are one
 // access where the address allows it (as two accesses of 16 bytes, 32 apart, they ran
 // slower than 8 elements a lane).  bf16 maxima and scaling run on packed pairs.
+// 92160 x 2880 bf16: quantize 98 us (6.8 TB/s), dequantize 117 us (5.8 TB/s); with 8 elements a
+// lane 246 us for both, now 222.  Activations into tiles, 16384 x 2880: 26 us (4.6 TB/s, of which
+// some 3 us are the launch's).
 //
 // Scale layouts.  "Rows": [rows, K/32], what the MXFP4 expert weights of the layer use.
 // "Tiles": what the 4-bit x 4-bit product reads: for 128 rows and 128 elements of K one
