@@ -42,13 +42,6 @@ __device__ __forceinline__ void pdl_enter() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// The same in two parts, for kernels that set up barriers and TMEM in between: nothing that
-// an earlier kernel may have written is read before pdl_wait.
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Host: launch `kern` on `stream` with programmatic stream serialization allowed.
 // Errors are left for cudaGetLastError, as with <<<>>>.
 template <typename... KArgs, typename... Args>
@@ -81,17 +74,6 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 }
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
-
-// One lane of a converged warp (the same one every time).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 
 // --------------------------------------------------------------------------
 // mbarrier

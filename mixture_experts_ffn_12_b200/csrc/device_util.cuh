@@ -1,0 +1,26 @@
+// Device helpers of the training and MXFP4 kernels, beside common.cuh.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// pdl_enter in two parts, for kernels that set up barriers and TMEM in between: nothing that
+// an earlier kernel may have written is read before pdl_wait.
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+}  // namespace moe

@@ -29,6 +29,7 @@
 //   below and above 128 for the first 128 elements, then for the others.
 #pragma once
 
+#include "device_util.cuh"
 #include "grouped_gemm_mx8.cuh"
 
 namespace moe {
