@@ -37,7 +37,8 @@
  *    library's kernels lets the next kernel on the stream be scheduled early and
  *    itself waits (griddepcontrol.wait) for the preceding kernel's completion and
  *    memory before touching any buffer, so stream order is kept for callers'
- *    kernels and copies before and after a call.
+ *    kernels and copies before and after a call.  (Within one call a kernel may
+ *    start beside the one before it, on buffers that one does not write.)
  *  - Arguments are validated before any launch; a rejected call launches
  *    nothing and returns MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED /
  *    MOE_ERR_WORKSPACE.  T = 0 is a successful no-op (expert_off is zeroed
@@ -49,7 +50,8 @@
  *    call are unspecified.
  *  - Supported sizes: 1 <= k <= min(E, 8), 1 <= E <= 256, D and F multiples of
  *    16 (of 32 for MXFP4), T >= 0 with T*k < 2^31; swiglu_limit finite and > 0.
- *  - NaN/Inf inputs: unspecified.
+ *  - NaN/Inf inputs: unspecified, but for the MXFP4 and training calls, which
+ *    say what becomes of them.
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
@@ -360,7 +362,7 @@ MOE_API moe_status_t moe_glm_layer_forward(const moe_config_t* cfg, const moe_gl
  * ------------------------------------------------------------------------ */
 
 /* MXFP4 quantization of rows along K, the format of the MOE_W_MXFP4 weights:
- *   x [rows, K] in dtype (moe_dtype_t; K a multiple of 32)
+ *   x [rows, K] in dtype (moe_dtype_t; K a multiple of 32, at most 2^20)
  *   -> codes [rows, K/2] uint8 E2M1 (element 2i = low nibble of byte i),
  *      scales [rows, K/32] uint8 E8M0: X + 127 for the block's scale 2^X, X the
  *      smallest integer >= -127 with max |x| of the block <= 6 * 2^X (no
@@ -395,7 +397,8 @@ MOE_API moe_status_t moe_mxfp4_weight_tiles(int32_t G, int32_t N, int32_t K, con
  *   x [R, K] bf16, w_codes [G, N, K/2], w_tiles from moe_mxfp4_weight_tiles,
  *   bias [G, N] bf16 or NULL -> out [R, N] bf16, or fp32 if out_f32 is 1.
  * Rows that belong to no group are left as they are.
- * 1 <= G <= 256, N a multiple of 16, K of 32.  ws:
+ * 1 <= G <= 256, N a multiple of 16, K of 32, both at most 2^20.  A row of x
+ * with an infinity or a NaN gives a row of NaN.  ws:
  * moe_mxfp4_linear_workspace_size bytes (the quantized activations). */
 MOE_API size_t moe_mxfp4_linear_workspace_size(int32_t G, int64_t R, int32_t N, int32_t K);
 MOE_API moe_status_t moe_mxfp4_linear(int32_t G, int64_t R, int32_t N, int32_t K, const void* x,
@@ -419,8 +422,10 @@ typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_SILU = 1 } moe_act_t;
  *      h [R, F] in dtype, y_perm [R, D] in dtype.
  * Dense weights in dtype; each of the biases may be NULL (none).  h_split and
  * MXFP4 weights: MOE_ERR_UNSUPPORTED.  With E = k = 1 it is a dense block.  Rows
- * that belong to no expert (behind expert_off[E]) are left as they are.  Not
- * touched by moe_set_expert_gemm_variant. */
+ * that belong to no expert (behind expert_off[E]) are left as they are.  A NaN
+ * passes the clips: it reaches every output of its row.  No output may overlap
+ * an input, here and in the backward pass.  Not touched by
+ * moe_set_expert_gemm_variant. */
 MOE_API moe_status_t moe_expert_ffn_train(const moe_config_t* cfg, int32_t act, int64_t T, const void* x_perm,
                                           const int32_t* expert_off, const moe_expert_weights_t* weights, void* gu,
                                           void* h, void* y_perm, void* stream);
@@ -450,6 +455,8 @@ typedef struct {
  * (tensor-core operands); every sum is fp32.  fp32 layers: fp32 FMA throughout.
  * The biases of `weights` are not read; their gradients are sums of dg and du as
  * they are before that rounding.  Deterministic.  T = 0 zeroes the gradients.
+ * A NaN or an infinity in a row stays with that row's dx and its expert's
+ * gradients; a NaN in g or u reaches them.
  * ws: moe_expert_ffn_backward_workspace_size bytes; on return it begins with
  * (dg, du) [R, 2, F] in dtype, as rounded. */
 MOE_API size_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, int64_t T);

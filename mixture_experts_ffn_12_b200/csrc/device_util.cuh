@@ -23,4 +23,11 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// v clipped into [lo, hi]; a NaN stays one (fminf and fmaxf would drop it, and a diverged
+// training step would go unseen).
+__device__ __forceinline__ float clip_nan(float v, float lo, float hi) {
+  asm("max.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;" : "+f"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+
 }  // namespace moe

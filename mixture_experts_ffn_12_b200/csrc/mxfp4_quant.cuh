@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(256) mx4_quant_tiles_kernel(const __nv_bfloat1
   const int kc = mx4_chunks(K);
   const int k_first = blockIdx.y * spans * kMx4QuantSpan;
   const int k_end = min(k_first + spans * kMx4QuantSpan, kc * 128);
-  const int step = gridDim.x * 8;
   constexpr int IT = kMx4QuantSpan / 512;
-  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += step) {
+  for (int64_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
+    const int row = static_cast<int>(r);
     const __nv_bfloat16* src = x + static_cast<size_t>(row) * K;
     uint2* crow = codes + (static_cast<size_t>(row) * K >> 4);
     uint8_t* dst = nullptr;

@@ -212,14 +212,15 @@ __device__ __forceinline__ float bf16_keep_side(float v, float lim) {
   return copysignf(__bfloat162float(__ushort_as_bfloat16(b)), v);
 }
 
-// Derivatives of h = f(clip(g)) clip(u) times dh.  The clips pass the gradient at their ends.
+// Derivatives of h = f(clip(g)) clip(u) times dh.  The clips pass the gradient at their ends,
+// and that of a NaN.
 __device__ __forceinline__ void act_grad(float dh, float g, float u, float limit, float alpha, float gate_lo,
                                          float& dg, float& du) {
-  const float gc = fminf(fmaxf(g, gate_lo), limit), uc = fminf(fmaxf(u, -limit), limit);
+  const float gc = clip_nan(g, gate_lo, limit), uc = clip_nan(u, -limit, limit);
   const float s = __fdividef(1.0f, 1.0f + __expf(-alpha * gc));
   const float f = gc * s;
-  dg = (g >= gate_lo && g <= limit) ? dh * uc * (s + alpha * f * (1.0f - s)) : 0.0f;
-  du = (u >= -limit && u <= limit) ? dh * f : 0.0f;
+  dg = (g < gate_lo || g > limit) ? 0.0f : dh * uc * (s + alpha * f * (1.0f - s));
+  du = fabsf(u) > limit ? 0.0f : dh * f;
 }
 
 struct TrainTile {
@@ -709,8 +710,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const float gv = v[j + q] + bias0, uv = u[j + q] + bias1;
-                const float gc = fminf(fmaxf(gv, args.gate_lo), args.limit);
-                const float uc = fminf(fmaxf(uv, -args.limit), args.limit);
+                const float gc = clip_nan(gv, args.gate_lo, args.limit);
+                const float uc = clip_nan(uv, -args.limit, args.limit);
                 h[q] = __fdividef(gc, 1.0f + __expf(-args.alpha * gc)) * uc;
                 g[q] = bf16_keep_side(gv, args.limit);
                 w[q] = bf16_keep_side(uv, args.limit);

@@ -165,6 +165,36 @@ def test_non_finite_rows_stay_with_their_expert(api, bad):
         assert torch.equal(clean[at], poisoned[at]), i
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", ["swiglu", "silu"])
+def test_nan_is_not_clipped_away(api, act, dtype):
+    """A NaN in a row of x reaches the whole row of gu, h and y; one in gu the row of dx, its feature's weight
+    gradients and those alone."""
+    D, F = 64, 48
+    b = Block([9, 40], D, F, dtype, True, seed=8)
+    b.x[3, 5] = float("nan")
+    cfg, gu, h, y = _forward(api, b, act)
+    for t in (gu, h, y):
+        assert torch.isnan(t[3]).all() and torch.isfinite(torch.cat([t[:3], t[4:]])).all()
+    b = Block([9, 40], D, F, dtype, True, seed=8)
+    cfg, gu, h, _ = _forward(api, b, act)
+    gu[3, 0, 7] = gu[20, 1, 11] = float("nan")
+    gu[3, 1, 7] = gu[20, 0, 11] = 0.5      # the other factor inside its clip
+    dx, gr = api.expert_ffn_backward(cfg, b.x, b.off_gpu, b.weights(api), gu, h, b.dy, act=act)
+    torch.cuda.synchronize()
+    assert api.last_device_error() == 0
+    rows = torch.isnan(dx).all(1)
+    assert rows.nonzero().flatten().tolist() == [3, 20] and torch.isfinite(dx[~rows]).all()
+    for grad, bias in ((gr.w_gate, gr.b_gate), (gr.w_up, gr.b_up)):
+        assert torch.equal(torch.isnan(grad).all(2), torch.isnan(bias))
+        for e, f in ((0, 7), (1, 11)):
+            bad = torch.isnan(bias[e])
+            assert set(bad.nonzero().flatten().tolist()) <= {f}
+    # d/dg at a NaN g, d/du at a NaN u: both; the other derivative holds the NaN factor as well
+    assert torch.isnan(gr.b_gate[0, 7]) and torch.isnan(gr.b_up[0, 7])
+    assert torch.isnan(gr.b_gate[1, 11])
+
+
 def test_partial_requests_and_reproducible(api):
     """Some gradients only, given buffers, a second call with the same bits; nothing else is written."""
     b = Block([70, 0, 131], 96, 176, BF16, True, seed=3)
