@@ -189,9 +189,11 @@ def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _rows_of(rows: int, n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-    """A new [rows, n] tensor (torch.empty takes 0.8 us longer to read its arguments)."""
-    return torch.empty_strided((rows, n), (n, 1), dtype=dtype, device=device)
+def _new(shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """A new contiguous tensor (torch.empty takes 0.8 us longer to read its arguments)."""
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _workspace(ws: Optional[torch.Tensor], n: int, device: torch.device) -> torch.Tensor:
@@ -506,8 +508,8 @@ def quantize_mxfp4(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     if K == 0 or K % 32:
         raise ValueError(f"quantize_mxfp4: the last dimension ({K}) must be a positive multiple of 32")
     lead = x.shape[:-1]
-    codes = x.new_empty((*lead, K // 2), dtype=torch.uint8)
-    scales = x.new_empty((*lead, K // 32), dtype=torch.uint8)
+    codes = _new((*lead, K // 2), torch.uint8, x.device)
+    scales = _new((*lead, K // 32), torch.uint8, x.device)
     _launch("moe_quantize_mxfp4", x.device, x.numel() // K, K, _DT_OF[x.dtype], x, codes, scales)
     return codes, scales
 
@@ -523,8 +525,9 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
     K = 2 * codes.shape[-1]
     if K == 0 or K % 32:
         raise ValueError(f"dequantize_mxfp4: K = {K} must be a positive multiple of 32")
-    _want("scales", scales, (*codes.shape[:-1], K // 32), torch.uint8, codes.device)
-    out = codes.new_empty((*codes.shape[:-1], K), dtype=dtype)
+    lead = codes.shape[:-1]
+    _want("scales", scales, (*lead, K // 32), torch.uint8, codes.device)
+    out = _new((*lead, K), dtype, codes.device)
     _launch("moe_dequantize_mxfp4", codes.device, out.numel() // K, K, codes, scales, _DT_OF[dtype], out)
     return out
 
@@ -586,7 +589,7 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] 
     G, N, K = _mxfp4_sizes(w.codes)
     L, dev = _lib.load(), x.device
     if y is None:
-        y = _rows_of(R, N, torch.float32 if out_f32 else torch.bfloat16, dev)
+        y = _new((R, N), torch.float32 if out_f32 else torch.bfloat16, dev)
     ws = _workspace(ws, _size(L.moe_mxfp4_linear_workspace_size(G, R, N, K), "moe_mxfp4_linear_workspace_size"), dev)
     _launch("moe_mxfp4_linear", dev, G, R, N, K, x, group_off, w.codes, w.tiles, bias, 1 if out_f32 else 0, y, ws,
             ws.numel() * ws.element_size())
@@ -655,7 +658,7 @@ def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Ten
     R, dev, dt = x_perm.shape[0], x_perm.device, x_perm.dtype
     F = cfg.intermediate_size
     gu = torch.empty_strided((R, 2, F), (2 * F, F, 1), dtype=dt, device=dev)
-    h = _rows_of(R, F, dt, dev)
+    h = _new((R, F), dt, dev)
     y = torch.empty_like(x_perm)
     wst = weights.c_struct()
     _launch("moe_expert_ffn_train", dev, ctypes.byref(cfg), code, T, x_perm, expert_off, ctypes.byref(wst), gu, h, y)

@@ -44,7 +44,7 @@ struct Mx4Layout {
   static constexpr int SFA_BYTES = 1024;          // 2 chunks of 128 K
   static constexpr int SFB_BYTES = 2048;          // 2 chunks of 128 K x 2 of 128 rows
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int EXTRA = 1024 + 3072;
+  static constexpr int EXTRA = 4096;   // alignment to 1024, barriers and tables
   static constexpr int SMEM = kMx4Stages * STAGE_BYTES + EXTRA;
   // TMEM: accumulators at columns 0 and 256; scales of even / odd stages behind them:
   // weights 2 chunks x 4 columns, then rows 2 chunks x 2 x 4 columns

@@ -12,7 +12,7 @@
 // 129 + 202 against 128 + 199 us at 1024 rows, 4 experts, D = F = 640 (20 TFLOP/s: larger
 // tiles would serve such layers better, which the small ones would pay for).
 // The weight gradients, whose K is an expert's few rows, are the other way about: few steps
-// and many outputs, one group and tiles of 64 x 128 (32 x 64 with four groups: 3072 CTAs of
+// and many outputs, one group and tiles of 64 x 128 (32 x 64 with four groups: four times the CTAs, of
 // one step each, 25 against 13 us).  An operand tile is kept in the order in which it lies in
 // memory, [row][K] (16-byte pieces along K) or [K][row] (along the rows), with 16 bytes of
 // padding a row; either way a thread takes 4 x 4 of it per four K steps with four 16-byte loads.

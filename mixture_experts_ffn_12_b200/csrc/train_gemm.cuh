@@ -97,7 +97,7 @@ struct TrainLayout {
   static constexpr int ONES = KIND == TR_DW ? 1024 : 0;   // 8 rows x 128 B of bf16 ones: half of N = 16
   static constexpr int STAGING_WARP = KIND == TR_DW ? 32 * 80 : 0;   // epilogue: 32 rows of 64 B + 16 B
   static constexpr int STAGING = kTrEpiWarps * STAGING_WARP;
-  static constexpr int EXTRA = 1024 + 3072;
+  static constexpr int EXTRA = 4096;   // alignment to 1024, barriers and tables
   static constexpr int SMEM = STAGES * STAGE_BYTES + ONES + STAGING + EXTRA;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
