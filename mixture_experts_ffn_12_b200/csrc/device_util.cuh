@@ -30,4 +30,22 @@ __device__ __forceinline__ float clip_nan(float v, float lo, float hi) {
   return v;
 }
 
+// The same into [-lim, lim].
+__device__ __forceinline__ float clip_nan(float v, float lim) {
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(v) : "f"(lim));
+  return v;
+}
+
+// 1 / (1 + 2^z) of two values, on the approximate units (2 ulp each): the results here are
+// rounded to bf16, or to 8 bits more for a sum.
+__device__ __forceinline__ float2 sigmoid2_neg_log2(float2 z) {
+  float2 e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+  e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+  return s;
+}
+
 }  // namespace moe

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
         const size_t bi = static_cast<size_t>(g) * jb.n + col;
         const float gv = jb.bias0 == nullptr ? v : v + jb.bias0[bi];
         const float uv = jb.bias1 == nullptr ? tot[S::kNB - 1][c] : tot[S::kNB - 1][c] + jb.bias1[bi];
-        const float gc = clip_nan(gv, args.gate_lo, args.limit), uc = clip_nan(uv, -args.limit, args.limit);
+        const float gc = clip_nan(gv, args.gate_lo, args.limit), uc = clip_nan(uv, args.limit);
         args.gu_out[orow * 2 * jb.n + col] = gv;
         args.gu_out[orow * 2 * jb.n + jb.n + col] = uv;
         jb.out[orow * jb.n + col] = gc / (1.0f + expf(-args.alpha * gc)) * uc;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kStThreads) simt_train_kernel(const SimtTrainA
         jb.out[orow * jb.n + col] = jb.bias0 == nullptr ? v : v + jb.bias0[static_cast<size_t>(g) * jb.n + col];
       } else if constexpr (KIND == SIMT_DH) {
         const float gv = args.gu[orow * 2 * jb.n + col], uv = args.gu[orow * 2 * jb.n + jb.n + col];
-        const float gc = clip_nan(gv, args.gate_lo, args.limit), uc = clip_nan(uv, -args.limit, args.limit);
+        const float gc = clip_nan(gv, args.gate_lo, args.limit), uc = clip_nan(uv, args.limit);
         const float s = 1.0f / (1.0f + expf(-args.alpha * gc)), f = gc * s;
         jb.out[orow * 2 * jb.n + col] =
             (gv < args.gate_lo || gv > args.limit) ? 0.0f : v * uc * (s + args.alpha * f * (1.0f - s));

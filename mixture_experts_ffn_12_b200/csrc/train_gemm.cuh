@@ -189,16 +189,16 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
 
 // A lane's values of one column in rows j (a) and j + 1 (b), rounded to bf16 and traded with
 // the neighbouring lane: the even lane gets both columns of row j, the odd one of row j + 1.
-__device__ __forceinline__ uint32_t trade_pair(float a, float b) {
+// `sel` is the lane's byte selector, trade_sel.
+__device__ __forceinline__ uint32_t trade_sel() { return (threadIdx.x & 1) ? 0x3276u : 0x5410u; }
+__device__ __forceinline__ uint32_t trade_pair(float a, float b, uint32_t sel) {
   const __nv_bfloat162 mine = __floats2bfloat162_rn(a, b);
   const uint32_t x = *reinterpret_cast<const uint32_t*>(&mine);
-  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
-  return (threadIdx.x & 1) ? __byte_perm(y, x, 0x7632) : __byte_perm(x, y, 0x5410);
+  return __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 1), sel);
 }
 // The way back: both columns of the lane's row to its own column in rows j and j + 1.
-__device__ __forceinline__ float2 untrade_pair(uint32_t x) {
-  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
-  const uint32_t z = (threadIdx.x & 1) ? __byte_perm(y, x, 0x7632) : __byte_perm(x, y, 0x5410);
+__device__ __forceinline__ float2 untrade_pair(uint32_t x, uint32_t sel) {
+  const uint32_t z = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 1), sel);
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&z));
 }
 
@@ -212,15 +212,21 @@ __device__ __forceinline__ float bf16_keep_side(float v, float lim) {
   return copysignf(__bfloat162float(__ushort_as_bfloat16(b)), v);
 }
 
-// Derivatives of h = f(clip(g)) clip(u) times dh.  The clips pass the gradient at their ends,
-// and that of a NaN.
-__device__ __forceinline__ void act_grad(float dh, float g, float u, float limit, float alpha, float gate_lo,
-                                         float& dg, float& du) {
-  const float gc = clip_nan(g, gate_lo, limit), uc = clip_nan(u, -limit, limit);
-  const float s = __fdividef(1.0f, 1.0f + __expf(-alpha * gc));
-  const float f = gc * s;
-  dg = (g < gate_lo || g > limit) ? 0.0f : dh * uc * (s + alpha * f * (1.0f - s));
-  du = fabsf(u) > limit ? 0.0f : dh * f;
+// Derivatives of h = f(clip(g)) clip(u) times dh, for two rows.  The clips pass the gradient
+// at their ends, and that of a NaN.
+__device__ __forceinline__ void act_grad(float2 dh, float2 g, float2 u, float limit, float alpha, float gate_lo,
+                                         float2& dg, float2& du) {
+  const float2 gc = make_float2(clip_nan(g.x, gate_lo, limit), clip_nan(g.y, gate_lo, limit));
+  const float2 uc = make_float2(clip_nan(u.x, limit), clip_nan(u.y, limit));
+  const float2 a2 = make_float2(alpha, alpha);
+  const float zl = -alpha * 1.44269504f;   // log2(e)
+  const float2 s = sigmoid2_neg_log2(__fmul2_rn(gc, make_float2(zl, zl)));
+  const float2 f = __fmul2_rn(gc, s);
+  const float2 rest = __ffma2_rn(s, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+  const float2 slope = __ffma2_rn(__fmul2_rn(a2, f), rest, s);
+  const float2 vg = __fmul2_rn(__fmul2_rn(dh, uc), slope), vu = __fmul2_rn(dh, f);
+  dg = make_float2((g.x < gate_lo || g.x > limit) ? 0.0f : vg.x, (g.y < gate_lo || g.y > limit) ? 0.0f : vg.y);
+  du = make_float2(fabsf(u.x) > limit ? 0.0f : vu.x, fabsf(u.y) > limit ? 0.0f : vu.y);
 }
 
 struct TrainTile {
@@ -382,14 +388,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     for (int i = threadIdx.x - 64; i < LY::ONES / 4; i += 128) reinterpret_cast<uint32_t*>(ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
   }
-  if (KIND != TR_DW || !args.early) pdl_wait();
-  if constexpr (KIND == TR_DX) pdl_launch_dependents();
-  if (warp == 0) group_table(args.group_off, G, args.m_total, args.tile_rows, goff, tile_off);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (KIND != TR_DW || !args.early) pdl_wait();
+  if constexpr (KIND == TR_DX) pdl_launch_dependents();
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const int KB1 = (args.k_dim + kTrBK - 1) / kTrBK;   // DX: K blocks of one half
 
@@ -415,6 +420,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
 
   if (warp == 2 + kTrEpiWarps) {
     // ------------------------------------------------------------ scheduler
+    group_table(args.group_off, G, args.m_total, args.tile_rows, goff, tile_off);
+    __syncwarp();   // the ring's barrier passes the table on with the first tile
     if (lane == 0) {
       int total = 0;
       if constexpr (KIND == TR_DW) {
@@ -674,7 +681,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
           if (cvalid && jb.bias0 != nullptr) bias0 = __bfloat162float(jb.bias0[bi]);
           if (KIND == TR_GATEUP && cvalid && jb.bias1 != nullptr) bias1 = __bfloat162float(jb.bias1[bi]);
         }
-        float sum_g = 0.0f, sum_u = 0.0f;   // DH: of this lane's column
+        const uint32_t sel = trade_sel();
+        float2 sum_g = {}, sum_u = {};      // DH: of this lane's column, even and odd rows
         uint32_t pg[8], pu[8];
         auto fetch = [&](int c) {
           if constexpr (KIND == TR_DH) {
@@ -711,12 +719,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
               for (int q = 0; q < 2; ++q) {
                 const float gv = v[j + q] + bias0, uv = u[j + q] + bias1;
                 const float gc = clip_nan(gv, args.gate_lo, args.limit);
-                const float uc = clip_nan(uv, -args.limit, args.limit);
+                const float uc = clip_nan(uv, args.limit);
                 h[q] = __fdividef(gc, 1.0f + __expf(-args.alpha * gc)) * uc;
                 g[q] = bf16_keep_side(gv, args.limit);
                 w[q] = bf16_keep_side(uv, args.limit);
               }
-              const uint32_t ph = trade_pair(h[0], h[1]), pgv = trade_pair(g[0], g[1]), puv = trade_pair(w[0], w[1]);
+              const uint32_t ph = trade_pair(h[0], h[1], sel), pgv = trade_pair(g[0], g[1], sel), puv = trade_pair(w[0], w[1], sel);
               if (c + j < rows) {
                 *reinterpret_cast<uint32_t*>(o) = ph;
                 *reinterpret_cast<uint32_t*>(p) = pgv;
@@ -726,22 +734,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
           } else if constexpr (KIND == TR_DH) {
             tmem_ld_wait();
             uint32_t dgs[8], dus[8];
+            if (c + 16 > ti.rows) {   // columns past the tile's rows hold other rows' products
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = c + j < ti.rows ? v[j] : 0.0f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float2 g = untrade_pair(pg[j]), u = untrade_pair(pu[j]);
-              float dg0, du0, dg1, du1;
-              act_grad(v[2 * j], g.x, u.x, args.limit, args.alpha, args.gate_lo, dg0, du0);
-              act_grad(v[2 * j + 1], g.y, u.y, args.limit, args.alpha, args.gate_lo, dg1, du1);
-              if (c + 2 * j < ti.rows) {   // accumulator columns past the tile's rows hold other rows' products
-                sum_g += dg0;
-                sum_u += du0;
-              }
-              if (c + 2 * j + 1 < ti.rows) {
-                sum_g += dg1;
-                sum_u += du1;
-              }
-              dgs[j] = trade_pair(dg0, dg1);
-              dus[j] = trade_pair(du0, du1);
+              float2 dg, du;
+              act_grad(make_float2(v[2 * j], v[2 * j + 1]), untrade_pair(pg[j], sel), untrade_pair(pu[j], sel),
+                       args.limit, args.alpha, args.gate_lo, dg, du);
+              sum_g = __fadd2_rn(sum_g, dg);
+              sum_u = __fadd2_rn(sum_u, du);
+              dgs[j] = trade_pair(dg.x, dg.y, sel);
+              dus[j] = trade_pair(du.x, du.y, sel);
             }
             fetch(c + 32);
             __nv_bfloat16* o = out + c * ld;
@@ -756,15 +761,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
             __nv_bfloat16* o = out + c * ld;
 #pragma unroll
             for (int j = 0; j < 16; j += 2, o += 2 * ld) {
-              const uint32_t both = trade_pair(v[j] + bias0, v[j + 1] + bias0);
+              const uint32_t both = trade_pair(v[j] + bias0, v[j + 1] + bias0, sel);
               if (c + j < rows) *reinterpret_cast<uint32_t*>(o) = both;
             }
           }
         }
         if (KIND == TR_DH && args.part != nullptr && cvalid && ti.rt < args.part_tiles) {
           float* p = args.part + static_cast<size_t>(2 * ti.rt + half) * args.part_ld + col;
-          p[0] = sum_g;
-          p[M] = sum_u;
+          p[0] = sum_g.x + sum_g.y;
+          p[M] = sum_u.x + sum_u.y;
         }
       }
       tc_fence_before();
