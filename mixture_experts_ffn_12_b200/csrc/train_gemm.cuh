@@ -59,12 +59,17 @@
 // accumulator buffers, and the closing cluster barrier of grouped_gemm_pair.cuh.
 //
 // Measured, 32 experts, D = F = 2880, 16384 rows, passes one after another: GATEUP 537 us
-// (1.01 PFLOP/s), DOWN 276 (0.99), DH 323 to 366 (0.74 to 0.84), DX 547 (0.99), DW 962 with bf16
+// (1.01 PFLOP/s), DOWN 276 (0.99), DH 323 to 385 (0.71 to 0.84), DX 547 (0.99), DW 962 with bf16
 // gradients (0.85).  Power bounds them: 990 W, 1.1 to 1.3 GHz of 1.965; a library product of the
 // same sizes in even groups runs at 0.95 to 1.09 there.  One launch alone at 1.6 GHz (8 experts,
-// 4096 rows) has the tensor pipe busy 67 / 58 / 39 / 64 / 62 % of the time.  DH's epilogue reads
-// g and u and writes dg and du, four values an element: without the stores it runs 16 % faster,
-// without the loads 22 %.
+// 4096 rows) has the tensor pipe busy 67 / 58 / 39 / 64 / 62 % of the time.
+// DH's epilogue takes 12 to 15 us for 256 rows where DOWN's takes 2: per value two operations
+// of the special-function unit and some 25 others (40 before the pairs of act_grad and the
+// lane selectors: 72 rows 6.2 us, now 4.2).  Its tile's MMAs take 19 us, so it shows in the last
+// tile of a launch, and where an expert has few columns.
+// Seven experts of 143 rows, D = 1440, F = 720 (49 us a backward pass): a launch takes 2 to 3 us
+// from the end of its wait to its first copy, 1.7 to the copy's arrival and 0.35 a stage, six
+// stages deep; DW's tiles there are bound by their epilogue, 2 us for 128 x 256 a CTA.
 // Single CTAs of 128 x 256 with the rows in M: DX 529 to 545 us, DH 296 to 305 and DW 947 to
 // 967 against 524 / 327 / 849 for the pairs of their time; halving DX's row tiles past one wave
 // of CTA pairs, an L2 prefetch of the weights, and staggered K orders in DW gained 1 % or lost.
