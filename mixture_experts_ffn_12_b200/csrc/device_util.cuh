@@ -23,6 +23,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Writes v to another CTA's shared memory and counts its 4 bytes on a barrier there
+// (addresses from mapa_shared).
+__device__ __forceinline__ void st_async(uint32_t addr, int v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+               : "memory");
+}
+
 // v clipped into [lo, hi]; a NaN stays one (fminf and fmaxf would drop it, and a diverged
 // training step would go unseen).
 __device__ __forceinline__ float clip_nan(float v, float lo, float hi) {

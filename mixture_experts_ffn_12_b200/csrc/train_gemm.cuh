@@ -36,10 +36,14 @@
 // workspace; DW adds an expert's tiles in order.  (Sums of the rounded values, by the same
 // ones, were off by up to twice as much where a sum cancels.)
 //
-// DW needs nothing of DX, whose last wave of tiles leaves CTA pairs idle.  So DX lets its
-// dependents go only once its own wait is over: what DH wrote is then complete, DW starts on
-// the pairs that DX has left, and waits for DX at its end instead, so that the call's last
-// kernel ends last.
+// Dependent launches.  A call's kernels but its last let their dependents go once their own
+// wait is over, so that everything before the call is complete when the second and third
+// start: their schedulers read the offsets and decode the first tiles at once, and the rest
+// waits for the kernel before.  DW needs nothing of DX, whose last wave of tiles leaves CTA
+// pairs idle: it starts on those (what DH wrote is complete when DX's wait is over) and waits
+// for DX at its end instead, so that the call's last kernel ends last.  Its pairs then start
+// at different times, so after their first tile they take tiles from a counter that DH has
+// zeroed, one ahead of their producers (a tile's result does not depend on who computes it).
 //
 // dg and du are rounded to bf16 between DH and the two products that read them (they are
 // tensor-core operands); all sums are fp32.
@@ -154,6 +158,7 @@ struct TrainArgs {
   int num_groups;
   int m_total;                // R
   int early;                  // DW: behind a DX launch, starts beside it
+  int* counter;               // DH (zeroes it), DW if early: tiles taken beyond the pairs' first ones
   int tile_rows;              // most rows in a tile's N: TrainLayout::ROWS, or a half or quarter (DW: DH's)
   int k_dim;                  // K (DX: of one half)
   __nv_bfloat16* gu;          // GATEUP (written), DH: [R, 2, F]
@@ -334,7 +339,7 @@ __device__ __forceinline__ void store_rows64(uint8_t* stage, T* out, size_t ldo,
 template <int KIND, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     ffn_train_kernel(const __grid_constant__ TrainArgs<KIND> args) {
-  if constexpr (KIND != TR_DX) pdl_launch_dependents();
+  if constexpr (KIND == TR_DOWN || KIND == TR_DW) pdl_launch_dependents();
   using LY = TrainLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -348,8 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
   uint64_t* sfull = tempty + 2;                 // scheduler ring
   uint64_t* sempty = sfull + kTrSched;
   uint64_t* drain = sempty + kTrSched;
-  TrainTile* ring = reinterpret_cast<TrainTile*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kTrSched);
+  uint64_t* taken = drain + 1;                  // DW: the leader's producer has the tile
+  uint64_t* boxed = taken + 1;                  // DW: the leader's choices for the other CTA
+  TrainTile* ring = reinterpret_cast<TrainTile*>(boxed + 2 * kTrSched);
+  int* box = reinterpret_cast<int*>(ring + kTrSched);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(box + 2 * kTrSched);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* never_flag = abort_flag + 1;
   int* tile_off = never_flag + 1;              // [G+1]
@@ -376,6 +384,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
       mbar_init(&sempty[q], 1 + (rank == 0 ? 1 : 0) + kTrEpiWarps + (KIND == TR_DH || KIND == TR_DW ? 1 : 0));   // who reads a tile
     }
     mbar_init(drain, 1);
+    mbar_init(taken, 1);
+    for (int q = 0; q < 2 * kTrSched; ++q) mbar_init(&boxed[q], 1);
     *abort_flag = 0;
     *never_flag = 0;
     fence_barrier_init();
@@ -398,8 +408,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
   cluster_sync_all();   // both CTAs' barriers are initialised before any signal between them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (KIND != TR_DW || !args.early) pdl_wait();
-  if constexpr (KIND == TR_DX) pdl_launch_dependents();
+  if (KIND == TR_GATEUP || KIND == TR_DH || (KIND == TR_DW && !args.early)) pdl_wait();
+  else if (KIND != TR_DW && warp != 2 + kTrEpiWarps) pdl_wait();
+  if ((KIND == TR_DX && warp != 2 + kTrEpiWarps) || KIND == TR_GATEUP || KIND == TR_DH) pdl_launch_dependents();
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const int KB1 = (args.k_dim + kTrBK - 1) / kTrBK;   // DX: K blocks of one half
 
@@ -434,8 +445,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
       } else {
         total = tile_off[G] * ((args.job[0].m + kTrBM - 1) / kTrBM);
       }
+      if (KIND == TR_DH && blockIdx.x == 0) *args.counter = 0;
+      const int pairs = gridDim.x >> 1;
       int n = 0;
-      for (int i = blockIdx.x >> 1;; i += gridDim.x >> 1, ++n) {
+      for (int i = blockIdx.x >> 1;; ++n) {
         TrainTile t;
         t.job = -1;
         if (i < total) t = train_tile<KIND>(i, tile_off, goff, args);
@@ -444,6 +457,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
         ring[q] = t;
         mbar_arrive(&sfull[q]);
         if (i >= total) break;
+        if (KIND == TR_DW && args.early) {
+          // A box is written again eight tiles on: by then the other CTA's epilogue, which the
+          // accumulators' barriers keep within three tiles of the issuer, has long read it.
+          const int b = n % (2 * kTrSched);
+          if (rank == 0) {
+            if (!mbar_wait(taken, n & 1, abort_flag, lim)) { ok = false; break; }
+            i = pairs + atomicAdd(args.counter, 1);
+            st_async(mapa_shared(smem_u32(&box[b]), 1), i, mapa_shared(smem_u32(&boxed[b]), 1));
+          } else {
+            mbar_arrive_expect_tx(&boxed[b], 4);
+            if (!mbar_wait_cluster(&boxed[b], (n / (2 * kTrSched)) & 1, abort_flag, lim)) { ok = false; break; }
+            i = box[b];
+          }
+        } else {
+          i += pairs;
+        }
       }
       if (!ok) {
         *abort_flag = 1;
@@ -465,6 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
         if (!next_tile(n, ti, true)) { ok = false; break; }
         uniform(ti);
         if (ti.job < 0) break;
+        if (KIND == TR_DW && leader) mbar_arrive(taken);
         const TrainJob& jb = args.job[ti.job];
         const int a_row = ti.m0 + rank * 128;
         const bool a_two = a_row + 128 <= (jb.m & ~63) || (jb.m & 63) == 0;

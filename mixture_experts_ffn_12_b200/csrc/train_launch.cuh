@@ -155,9 +155,9 @@ static int train_tile_rows(const Launch& L, int64_t R, int E, int n, int most) {
 }
 
 // Workspace of the backward pass: dgu [R, 2, F], then (bf16) the sums of dg and du by row tile
-// (of 64 rows at least) and epilogue half.
+// (of 64 rows at least) and epilogue half, and the weight gradients' tile counter.
 struct BackwardLayout {
-  size_t part, total;
+  size_t part, counter, total;
 };
 static BackwardLayout backward_layout(bool bf16, int64_t R, int F, int E) {
   BackwardLayout l{};
@@ -165,7 +165,8 @@ static BackwardLayout backward_layout(bool bf16, int64_t R, int F, int E) {
   l.total = l.part;
   if (bf16) {
     l.part = (l.part + 255) / 256 * 256;
-    l.total = l.part + static_cast<size_t>((R + 63) / 64 + E) * 2 * 2 * F * 4;
+    l.counter = l.part + static_cast<size_t>((R + 63) / 64 + E) * 2 * 2 * F * 4;
+    l.total = l.counter + 16;
   }
   return l;
 }
@@ -224,6 +225,7 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   void* dgu = ws;
   float* part = (gr.b_gate != nullptr || gr.b_up != nullptr) ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + LY.part)
                                                              : nullptr;
+  int* counter = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + LY.counter);
   const int dh_rows = train_tile_rows(L, R, E, F, TrainLayout<TR_DH>::ROWS);
   const int part_tiles = static_cast<int>((R + dh_rows - 1) / dh_rows + E);
   __nv_bfloat16* dg = static_cast<__nv_bfloat16*>(dgu);
@@ -238,6 +240,7 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
     a.part = part;
     a.part_tiles = part_tiles;
     a.part_ld = 2 * F;
+    a.counter = counter;
     if ((e = launch_rows(L, a, R, E, F)) != cudaSuccess) return e;
   }
   if (dx != nullptr) {
@@ -254,6 +257,7 @@ static cudaError_t expert_backward_bf16(const Launch& L, int64_t R, int D, int F
   TrainArgs<TR_DW> a = train_args<TR_DW>(L, R, E, 0, off, act);
   a.num_jobs = 0;
   a.early = dx != nullptr;
+  a.counter = counter;
   a.tile_rows = dh_rows;
   a.part_tiles = part_tiles;
   a.part_ld = 2 * F;

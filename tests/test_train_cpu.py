@@ -104,8 +104,9 @@ def test_backward(lib):
     for bad in (dict(c=cfg(wfmt=_lib.MOE_W_MXFP4)), dict(c=cfg(h_split=1))):
         assert call(**bad) == UNS, bad
     need = lib.moe_expert_ffn_backward_workspace_size(cfg(), 3)
-    # dgu, rounded up to 256 bytes, then the bias sums of up to ceil(R / 64) + E row tiles, two halves each
-    assert need == 2304 + (1 + 4) * 2 * 2 * 96 * 4
+    # dgu, rounded up to 256 bytes, then the bias sums of up to ceil(R / 64) + E row tiles, two halves each, and
+    # a counter
+    assert need == 2304 + (1 + 4) * 2 * 2 * 96 * 4 + 16
     assert lib.moe_expert_ffn_backward_workspace_size(cfg(dtype=_lib.MOE_F32), 3) == 6 * 2 * 96 * 4
     assert lib.moe_expert_ffn_backward_workspace_size(cfg(h_split=1), 3) == _lib.SIZE_INVALID
     for bad in (dict(ws=None), dict(ws=ODD), dict(n=need - 1)):
