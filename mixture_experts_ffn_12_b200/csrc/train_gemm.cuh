@@ -69,11 +69,13 @@
 // 4096 rows) has the tensor pipe busy 67 / 58 / 39 / 64 / 62 % of the time.
 // DH's epilogue takes 12 to 15 us for 256 rows where DOWN's takes 2: per value two operations
 // of the special-function unit and some 25 others (40 before the pairs of act_grad and the
-// lane selectors: 72 rows 6.2 us, now 4.2).  Its tile's MMAs take 19 us, so it shows in the last
+// lane selectors: tiles of 48 rows, one a launch, 6.2 us, then 4.2, and 2.9 with its
+// instructions fetched before).  A 256-row tile's MMAs take 19 us, so it shows in the last
 // tile of a launch, and where an expert has few columns.
-// Seven experts of 143 rows, D = 1440, F = 720 (49 us a backward pass): a launch takes 2 to 3 us
-// from the end of its wait to its first copy, 1.7 to the copy's arrival and 0.35 a stage, six
-// stages deep; DW's tiles there are bound by their epilogue, 2 us for 128 x 256 a CTA.
+// Seven experts of 143 rows, D = 1440, F = 720 (43 us a backward pass): DH takes 2.5 us from
+// the end of its wait to its first copy, DX 0.4 (see above); then 1.5 to the copy's arrival and
+// 0.35 a stage, six stages deep; DW's tiles there are bound by their epilogue, 2 us for
+// 128 x 256 a CTA (4 TB/s of stores).
 // Single CTAs of 128 x 256 with the rows in M: DX 529 to 545 us, DH 296 to 305 and DW 947 to
 // 967 against 524 / 327 / 849 for the pairs of their time; halving DX's row tiles past one wave
 // of CTA pairs, an L2 prefetch of the weights, and staggered K orders in DW gained 1 % or lost.
@@ -647,9 +649,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     // Two warps share a TMEM lane quarter and take its column chunks in turn.
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    TrainTile ti;
-    for (int n = 0;; ++n) {
-      if (!next_tile(n, ti, true)) { ok = false; break; }
+    // DH's epilogue begins with a tile that has no rows of its own: a first pass over its 900
+    // instructions fetches them while the first operands are on their way (ragged SiLU backward
+    // 44.6 -> 42.9 us; GATEUP gains nothing by it).
+    TrainTile ti{};
+    ti.rows = 32;
+    for (int n = KIND == TR_DH ? -1 : 0;; ++n) {
+      const bool dry = n < 0;
+      if (!dry && !next_tile(n, ti, true)) { ok = false; break; }
       if (ti.job < 0) break;
       const TrainJob& jb = args.job[ti.job];
       const int acc = n & 1;
@@ -701,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
         // of two rows.  DH's g and u of the next 16 rows are on their way while these are
         // computed, the first before the accumulator is complete.
         const int col = row0 + lane, M = jb.m;
-        const bool cvalid = col < M;                          // M is a multiple of 16: of both lanes
+        const bool cvalid = col < M && !dry;                  // M is a multiple of 16: of both lanes
         constexpr int kRowElems = KIND == TR_DH ? 2 : 1;      // DH: [R, 2, F]
         const size_t ld = static_cast<size_t>(kRowElems) * M;
         const int odd = lane & 1;
@@ -733,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
           }
         };
         fetch(16 * half);
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
+        if (!dry && !__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (n >> 1) & 1, abort_flag, lim))) { ok = false; break; }
         tc_fence_after();
 #pragma unroll 1
         for (int c = 16 * half; c < ti.rows; c += 32) {
@@ -809,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc) * 8u);
+      if (lane == 0 && !dry) mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc) * 8u);
     }
     if (!ok) {
       *abort_flag = 1;
