@@ -210,6 +210,26 @@ def test_partial_requests_and_reproducible(api):
     assert torch.equal(dx, dx2) and torch.equal(full.b_up, again.b_up) and torch.equal(full.w_up, again.w_up)
 
 
+@pytest.mark.parametrize("need_dx", [True, False])
+def test_workspace_content_does_not_matter(api, need_dx):
+    """Calls one after another on one workspace, each time filled with other bytes (tile counter and bias sums lie
+    in it), give the same bits as a call on its own."""
+    b = Block([143, 0, 70, 300, 1], 200 - 200 % 16, 368, BF16, True, seed=9)
+    cfg, gu, h, _ = _forward(api, b, "swiglu")
+    w = b.weights(api)
+    dx, want = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy, need_dx=need_dx)
+    ws, _ = backward_ws(cfg, b)
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        for _ in range(3):
+            dx2, got = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy, need_dx=need_dx, ws=ws)
+            assert (dx is None) == (dx2 is None) and (dx is None or torch.equal(dx, dx2))
+            for n in ("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down"):
+                assert torch.equal(getattr(got, n), getattr(want, n)), (fill, n)
+    torch.cuda.synchronize()
+    assert api.last_device_error() == 0
+
+
 def test_rows_of_no_expert_are_left(api):
     """expert_off ends before the last row: the rows behind it are neither read into a gradient nor written."""
     b = Block([33, 20], 64, 48, BF16, True, seed=4)
