@@ -216,11 +216,14 @@ __device__ __forceinline__ float2 untrade_pair(uint32_t x, uint32_t sel) {
 
 // v rounded to bf16, kept on its side of the bounds +-lim: the backward pass decides from the
 // stored value whether the clip let the gradient through, so rounding must not move it across.
-__device__ __forceinline__ float bf16_keep_side(float v, float lim) {
+// The gate's lower bound is lo = 0 (-inf: none): a negative value too small for bf16 stays at
+// the smallest negative one instead of becoming -0, which lies inside the clip.
+__device__ __forceinline__ float bf16_keep_side(float v, float lim, float lo = -INFINITY) {
   const float a = fabsf(v);
   uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(a));
   const bool over = a > lim;
   if ((__bfloat162float(__ushort_as_bfloat16(b)) > lim) != over) b += over ? 1 : -1;
+  if (v < lo && b == 0) b = 1;
   return copysignf(__bfloat162float(__ushort_as_bfloat16(b)), v);
 }
 
@@ -763,7 +766,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
                 const float gc = clip_nan(gv, args.gate_lo, args.limit);
                 const float uc = clip_nan(uv, args.limit);
                 h[q] = __fdividef(gc, 1.0f + __expf(-args.alpha * gc)) * uc;
-                g[q] = bf16_keep_side(gv, args.limit);
+                g[q] = bf16_keep_side(gv, args.limit, args.gate_lo);
                 w[q] = bf16_keep_side(uv, args.limit);
               }
               const uint32_t ph = trade_pair(h[0], h[1], sel), pgv = trade_pair(g[0], g[1], sel), puv = trade_pair(w[0], w[1], sel);
