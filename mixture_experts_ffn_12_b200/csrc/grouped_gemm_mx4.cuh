@@ -101,6 +101,21 @@ struct Mx4Tile {
   int xt;               // row tile (of the scales)
 };
 
+// Waits for the copies counted on `stages` barriers (bit q of `issued`: some on barrier q, in the
+// phase that bit q of `par` says), also after a wait that gave up: a copy must not land in
+// shared memory that the CTA has left.  kDrainLimitNs from t0 on for all of them, since a
+// stage whose other copies were never issued does not complete.
+__device__ __forceinline__ bool wait_landed(uint64_t* bars, int stages, uint32_t issued, uint32_t par,
+                                            volatile int* never, uint64_t t0) {
+  bool all = true;
+  for (int q = 0; q < stages; ++q) {
+    if (!((issued >> q) & 1u)) continue;
+    const uint64_t gone = global_timer_ns() - t0;
+    all &= mbar_wait(&bars[q], (par >> q) & 1u, never, gone < kDrainLimitNs ? kDrainLimitNs - gone : 1);
+  }
+  return all;
+}
+
 template <typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     grouped_gemm_mx4_kernel(const __grid_constant__ Mx4Args args) {
@@ -264,9 +279,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
         }
         if (!ok) break;
       }
-      // every copy has landed before the CTA may leave (after a wait that gave up: see the end)
-      for (int q = 0; leader && rank == 0 && ok && q < kMx4Stages; ++q)
-        if ((issued >> q) & 1u) ok = mbar_wait(&full[q], (issued_par >> q) & 1u, abort_flag, kDrainLimitNs);
+      // every copy has landed before the CTA may leave (those counted on the peer's barriers: see the end)
+      if (leader && rank == 0 && !wait_landed(full, kMx4Stages, issued, issued_par, never_flag, global_timer_ns())) ok = false;
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
@@ -279,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
       const bool leader = elect_one();
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       int s = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, issued = 0, issued_par = 0;
       Mx4Tile ti;
       pdl_wait();   // the quantizer's codes and scales
       for (int n = 0;; ++n) {
@@ -297,10 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
             tma_load_2d_pair(st + LY::B_BYTES + LY::SFA_BYTES, &args.sx, fb, 0, xrow + kb * (LY::SFB_BYTES / 256));
           }
           __syncwarp();
+          issued |= 1u << s;
+          issued_par = (issued_par & ~(1u << s)) | (ph << s);
           if (++s == kMx4Stages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
       }
+      if (leader && rank == 0 && !wait_landed(full, kMx4Stages, issued, issued_par, never_flag, global_timer_ns())) ok = false;
       if (!ok) {
         *abort_flag = 1;
         flag_error(DEVERR_TIMEOUT);
@@ -434,8 +451,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
 
   tc_fence_before();
   __syncthreads();
-  // A role that gave up leaves copies in flight whose barrier nobody waits for any more: both
-  // CTAs stay until they have landed (the peer waits for this one at the cluster barrier).
+  // A role that gave up may leave copies in flight that count on the peer's barriers, which cannot
+  // be polled from here, or on a stage that does not complete: both CTAs give them 2 ms to land
+  // (the peer waits for this one at the cluster barrier).
   if (threadIdx.x == 0 && *abort_flag)
     for (int q = 0; q < 2000; ++q) __nanosleep(1000);
   cluster_sync_all();   // no CTA leaves while its peer may still signal it or read its memory

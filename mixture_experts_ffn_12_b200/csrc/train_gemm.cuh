@@ -565,10 +565,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
         }
         if (!ok) break;
       }
-      // every copy has landed before the CTA may leave (after a wait that gave up: see the end)
-      for (int q = 0; leader && ok && q < LY::STAGES; ++q) {
-        if (rank == 0 && ((issued >> q) & 1u)) ok = mbar_wait(&full[q], (issued_par >> q) & 1u, abort_flag, kDrainLimitNs);
-        if (ok && ((tails >> q) & 1u)) ok = mbar_wait(&landed[q], (tail_par >> q) & 1u, abort_flag, kDrainLimitNs);
+      // every copy has landed before the CTA may leave (those counted on the peer's barriers: see the end)
+      if (leader) {
+        const uint64_t t0 = global_timer_ns();
+        if (rank == 0 && !wait_landed(full, LY::STAGES, issued, issued_par, never_flag, t0)) ok = false;
+        if (!wait_landed(landed, LY::STAGES, tails, tail_par, never_flag, t0)) ok = false;
       }
       if (!ok) {
         *abort_flag = 1;
@@ -877,8 +878,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  // A role that gave up leaves copies in flight whose barrier nobody waits for any more: both
-  // CTAs stay until they have landed (the peer waits for this one at the cluster barrier).
+  // A role that gave up may leave copies in flight that count on the peer's barriers, which cannot
+  // be polled from here, or on a stage that does not complete: both CTAs give them 2 ms to land
+  // (the peer waits for this one at the cluster barrier).
   if (threadIdx.x == 0 && *abort_flag)
     for (int q = 0; q < 2000; ++q) __nanosleep(1000);
   if (KIND == TR_DW && args.early) pdl_wait();

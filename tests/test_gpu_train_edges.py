@@ -51,3 +51,48 @@ def test_gate_next_to_its_lower_bound(api, x0, w0, b0, g, act):
     else:
         assert (got == torch.tensor(g, dtype=F32).to(BF16).double().item()).all()
         assert (gr.b_gate != 0).all()                               # f'(0) = 1/2; f' > 0 at -1 as well
+
+
+def test_waits_that_run_out_with_several_tiles_a_pair(api):
+    """With a wait limit of 1 ns every kernel that has several tiles a CTA pair gives up: the calls return soon, the
+    error word says so, and the next calls on the same buffers have the right bits."""
+    import time
+    from mixture_experts_ffn_12_b200 import _lib
+    from train_util import Block
+    b = Block([700, 0, 1300, 345, 90], 2880, 2048, BF16, True, seed=11)
+    cfg, w = b.config(api), b.weights(api)
+    gen = torch.Generator("cuda").manual_seed(11)
+    codes = torch.randint(0, 256, (5, 2048, 2880), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.randint(119, 128, (5, 2048, 180), dtype=torch.uint8, device="cuda", generator=gen)
+    mw = api.mxfp4_weights(codes, scales)
+    x2 = torch.randn(b.R, 5760, device="cuda", generator=gen).to(BF16)
+    gu, h, y = api.expert_ffn_train(cfg, b.x, b.off_gpu, w)
+
+    def forward():
+        return list(api.expert_ffn_train(cfg, b.x, b.off_gpu, w))
+
+    def backward():
+        dx, gr = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy)
+        return [dx, gr.w_gate, gr.w_up, gr.w_down, gr.b_gate, gr.b_up, gr.b_down]
+
+    def linear():
+        return [api.mxfp4_linear(x2, mw, None, b.off_gpu)]
+    for call in (forward, backward, linear):
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        assert api.last_device_error() == 0
+        api.set_wait_limit_ns(1)
+        t0 = time.monotonic()
+        try:
+            call()
+            torch.cuda.synchronize()
+            status = api.last_device_error()
+        finally:
+            api.set_wait_limit_ns(0)
+        assert status == _lib.MOE_ERR_TIMEOUT, call.__name__
+        assert time.monotonic() - t0 < 30          # three launches, each drained within a few seconds
+        got = call()
+        torch.cuda.synchronize()
+        assert api.last_device_error() == 0
+        for a, c in zip(got, want):
+            assert torch.equal(a, c), call.__name__
