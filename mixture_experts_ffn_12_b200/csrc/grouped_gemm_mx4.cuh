@@ -185,16 +185,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // The next tile from the scheduler's ring; false when a wait gave up.  One thread, or a
-  // whole warp (which then agrees on the answer).
-  auto next_tile = [&](int n, Mx4Tile& t, bool whole_warp) {
+  // The next tile from the scheduler's ring; false when a wait gave up.  For a whole
+  // warp, which agrees on the answer.
+  auto next_tile = [&](int n, Mx4Tile& t) {
     const int q = n % kMx4Sched;
-    bool got = mbar_wait(&rfull[q], (n / kMx4Sched) & 1, abort_flag, lim);
-    if (whole_warp) got = __all_sync(0xffffffffu, got);
-    if (!got) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&rfull[q], (n / kMx4Sched) & 1, abort_flag, lim))) return false;
     t = ring[q];
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(&rempty[q]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&rempty[q]);
     return true;
   };
   // A tile that the whole warp has read, as values the compiler knows to be the same in every lane.
@@ -255,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
       uint32_t ph = 0, issued = 0, issued_par = 0;
       Mx4Tile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, true)) { ok = false; break; }
+        if (!next_tile(n, ti)) { ok = false; break; }
         uniform(ti);
         if (ti.g < 0) break;
         const int q32 = (ti.n + 63) / 64;                  // boxes of 32 rows in half of the rows
@@ -297,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
       Mx4Tile ti;
       pdl_wait();   // the quantizer's codes and scales
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, true)) { ok = false; break; }
+        if (!next_tile(n, ti)) { ok = false; break; }
         uniform(ti);
         if (ti.g < 0) break;
         const CUtensorMap* tx = &args.x[(ti.n + 63) / 64 - 1];
@@ -339,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
       bool issued_any = false;
       Mx4Tile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, true)) { ok = false; break; }
+        if (!next_tile(n, ti)) { ok = false; break; }
         uniform(ti);
         if (ti.g < 0) break;
         const int acc = n & 1;
@@ -402,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMx4Threads, 1)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     Mx4Tile ti;
     for (int n = 0;; ++n) {
-      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (!next_tile(n, ti)) { ok = false; break; }
       if (ti.g < 0) break;
       const int acc = n & 1;
       const int col = ti.m0 + rank * 128 + quarter * 32 + lane;

@@ -171,13 +171,6 @@ struct TrainArgs {
   unsigned long long wait_limit_ns;
 };
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const void* tmap, uint32_t bar_cluster, int c0, int c1,
                                                  int c2, int c3) {
   asm volatile(
@@ -419,16 +412,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const int KB1 = (args.k_dim + kTrBK - 1) / kTrBK;   // DX: K blocks of one half
 
-  // The next tile from the scheduler's ring; false when a wait gave up.  One thread, or a
-  // whole warp (which then agrees on the answer).
-  auto next_tile = [&](int n, TrainTile& t, bool whole_warp) {
+  // The next tile from the scheduler's ring; false when a wait gave up.  For a whole
+  // warp, which agrees on the answer.
+  auto next_tile = [&](int n, TrainTile& t) {
     const int q = n % kTrSched;
-    bool got = mbar_wait(&sfull[q], (n / kTrSched) & 1, abort_flag, lim);
-    if (whole_warp) got = __all_sync(0xffffffffu, got);
-    if (!got) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sfull[q], (n / kTrSched) & 1, abort_flag, lim))) return false;
     t = ring[q];
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(&sempty[q]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sempty[q]);
     return true;
   };
   // A tile that the whole warp has read, as values the compiler knows to be the same in every lane.
@@ -496,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
       uint32_t tails = 0, tail_par = 0, tail_uses = 0;     // stages counted on this CTA's landed
       TrainTile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, true)) { ok = false; break; }
+        if (!next_tile(n, ti)) { ok = false; break; }
         uniform(ti);
         if (ti.job < 0) break;
         if (KIND == TR_DW && leader) mbar_arrive(taken);
@@ -595,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
       bool issued_any = false;
       TrainTile ti;
       for (int n = 0;; ++n) {
-        if (!next_tile(n, ti, true)) { ok = false; break; }
+        if (!next_tile(n, ti)) { ok = false; break; }
         uniform(ti);
         if (ti.job < 0) break;
         const uint32_t idesc = make_idesc(kTrBM, ti.n, 1u) | (LY::A_KMAJOR ? 0u : 1u << 15) | (KIND == TR_DW ? 1u << 16 : 0u);
@@ -660,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     ti.rows = 32;
     for (int n = KIND == TR_DH ? -1 : 0;; ++n) {
       const bool dry = n < 0;
-      if (!dry && !next_tile(n, ti, true)) { ok = false; break; }
+      if (!dry && !next_tile(n, ti)) { ok = false; break; }
       if (ti.job < 0) break;
       const TrainJob& jb = args.job[ti.job];
       const int acc = n & 1;
@@ -831,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     // g and u of coming tiles into the L2: the epilogue's loads look only 16 rows ahead.
     TrainTile ti;
     for (int n = 0;; ++n) {
-      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (!next_tile(n, ti)) { ok = false; break; }
       if (ti.job < 0) break;
       const int F = args.job[0].m;
       const int col = ti.m0 + rank * 128 + (lane & 1) * 64;
@@ -852,7 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     uint32_t uses = 0;
     TrainTile ti;
     for (int n = 0;; ++n) {
-      if (!next_tile(n, ti, true)) { ok = false; break; }
+      if (!next_tile(n, ti)) { ok = false; break; }
       if (ti.job < 0) break;
       if (ti.kb > 0 && train_ragged(ti)) {
         const int q = (s + ti.kb - 1) % LY::STAGES;
