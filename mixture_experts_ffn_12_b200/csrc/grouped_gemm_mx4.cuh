@@ -23,8 +23,10 @@
 // grouped_gemm_pair.cuh.
 //
 // Measured, 32 groups, N = K = 2880: 16384 rows 78 us (3.5 PFLOP/s, tensor pipe busy 50 % of
-// the time, 237 MB from and to HBM; bound by power when passes follow one another), 128 rows
-// 24 us (5.9 TB/s of weights: HBM).  Single CTAs with the rows in M took 125 and 41 us.
+// the time, 237 MB from and to HBM), 128 rows 24 us (5.9 TB/s of weights: HBM).  At 16384 rows one
+// launch alone, at 1.6 to 1.9 GHz, is not bound by power: at the tensor pipe's nominal rate a
+// stage's 31 KB a CTA in 384 cycles would ask some 21 TB/s of the L2, more than it was seen to give
+// (15.5), and a wider tile has no room in TMEM beside two scale sets.  Single CTAs with the rows in M took 125 and 41 us.
 #pragma once
 
 #include "mxfp4_quant.cuh"

@@ -45,12 +45,18 @@
 // at different times, so after their first tile they take tiles from a counter that DH has
 // zeroed, one ahead of their producers (a tile's result does not depend on who computes it).
 //
-// dg and du are rounded to bf16 between DH and the two products that read them (they are
-// tensor-core operands); all sums are fp32.
+// Roundings to bf16: g and u as kept for the backward pass (bf16_keep_side); h, an output and the
+// down product's operand; dg and du between DH and the two products that read them.  The last
+// two are tensor-core operands, at the rate that the whole pass is about, and the layer's own
+// forward pass rounds h alike.  Against the formulas in 64 bits they put the relative error of
+// y, of dx and of the gate and up gradients at 2.3e-3 where one rounding of the result has
+// 1.7e-3; two bf16 halves of each would double the products that read them.  All sums are fp32.
 //
 // CTA pairs (cta_group::2): a tile of M = 256 x N <= 256 a pair, every CTA staging its own 128
 // rows of A and half of B, 32 KB a 64-deep stage where a CTA alone takes 48 KB for the same
-// MMA time.  DW's columns are split into blocks of 256 and 128 (narrow ones first), so that
+// MMA time.  N is a multiple of 16 from 16 on: each CTA then holds whole groups of eight rows of B,
+// and an expert of a few rows pays for no more than 16 (every width is compared in the tests).
+// DW's columns are split into blocks of 256 and 128 (narrow ones first), so that
 // every box row is one 128-byte line.
 //
 // Roles (384 threads a CTA): warp 0 TMA producer; warp 1 TMEM and, in the leader, the MMA
@@ -64,14 +70,16 @@
 //
 // Measured, 32 experts, D = F = 2880, 16384 rows, passes one after another: GATEUP 537 us
 // (1.01 PFLOP/s), DOWN 276 (0.99), DH 323 to 385 (0.71 to 0.84), DX 547 (0.99), DW 962 with bf16
-// gradients (0.85).  Power bounds them: 990 W, 1.1 to 1.3 GHz of 1.965; a library product of the
-// same sizes in even groups runs at 0.95 to 1.09 there.  One launch alone at 1.6 GHz (8 experts,
-// 4096 rows) has the tensor pipe busy 67 / 58 / 39 / 64 / 62 % of the time.
-// DH's epilogue takes 12 to 15 us for 256 rows where DOWN's takes 2: per value two operations
-// of the special-function unit and some 25 others (40 before the pairs of act_grad and the
-// lane selectors: tiles of 48 rows, one a launch, 6.2 us, then 4.2, and 2.9 with its
-// instructions fetched before).  A 256-row tile's MMAs take 19 us, so it shows in the last
-// tile of a launch, and where an expert has few columns.
+// gradients (0.85).  Such runs sit at the power limit (990 W, 1.1 to 1.3 GHz of 1.965), where a
+// library product of the same sizes in even groups runs at 0.95 to 1.09.  Power is not all of it:
+// one launch alone at 1.6 GHz (8 experts, 4096 rows) has the tensor pipe busy 67 / 58 / 39 / 64 /
+// 62 % of the time.  GATEUP's two accumulators of N <= 128 stage 40 KB for the MMA time of DOWN's 32.
+// DH, with DOWN's operations, takes 47 to 109 us longer: its epilogue also reads g and u and
+// writes dg and du, 378 MB in four-byte accesses.  Of 323 us, 253 are left without the loads of
+// g and u, 271 without the stores, 286 without the activation's instructions (each taken out
+// alone): the loads cost the most.  The epilogue takes 12 to 15 us for 256 rows where DOWN's takes
+// 2 (tiles of 48 rows, one a launch: 6.2 us, 4.2 with the pairs of act_grad and the lane selectors,
+// 2.9 with its instructions fetched before); a 256-row tile's MMAs take 19 us.
 // Seven experts of 143 rows, D = 1440, F = 720 (43 us a backward pass): DH takes 2.5 us from
 // the end of its wait to its first copy, DX 0.4 (see above); then 1.5 to the copy's arrival and
 // 0.35 a stage, six stages deep; DW's tiles there are bound by their epilogue, 2 us for
@@ -646,7 +654,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTrThreads, 1)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     // DH's epilogue begins with a tile that has no rows of its own: a first pass over its 900
     // instructions fetches them while the first operands are on their way (ragged SiLU backward
-    // 44.6 -> 42.9 us; GATEUP gains nothing by it).
+    // 44.6 -> 42.9 us; GATEUP gains nothing by it).  Its loads from the second accumulator are in no
+    // order with the second tile's MMAs, which may be writing there: what they bring is dropped.
     TrainTile ti{};
     ti.rows = 32;
     for (int n = KIND == TR_DH ? -1 : 0;; ++n) {

@@ -144,10 +144,12 @@ static TrainArgs<KIND> train_args(const Launch& L, int64_t R, int E, int k_dim, 
 
 static int64_t train_col_tiles(int n) { return (n + kTrBM - 1) / kTrBM; }
 
-// Rows of a tile: the most the kernel takes, halved (to 64 at least) while even experts'
-// tiles would not fill half of the CTA pairs, so that the halves still run at once.
-// (Backward of 7 experts of 143 rows, D = 1440, F = 720, 74 pairs: DH, 24 full tiles,
-// 22.2 us, halved 17.2; DX, 48 full tiles, 15.4 us, halved -- more than a wave -- 20.1.)
+// Rows of a tile: the most the kernel takes, halved (to 64 at least) while the tiles of evenly
+// loaded experts would not fill half of the CTA pairs, so that the halves still run at once.
+// The host does not know the loads: the estimate gives every expert, empty ones too, the
+// average.  (Backward of 8 experts, seven of 143 rows and one empty, D = 1440, F = 720, 74 pairs:
+// DH, 24 full tiles by the estimate and 21 in fact, 22.2 us, is quartered to at most 64 rows, 63
+// tiles of 48, 17.2 us; DX, 48 and 42, stays full, 15.4 us -- halved, more than a wave, 20.1.)
 static int train_tile_rows(const Launch& L, int64_t R, int E, int n, int most) {
   const int64_t avg = std::max<int64_t>(1, (R + E - 1) / E), experts = std::min<int64_t>(E, R);
   while (most > 64 && 2 * experts * ((avg + most - 1) / most) * train_col_tiles(n) <= L.num_sms / 2) most /= 2;
