@@ -417,9 +417,11 @@ typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_SILU = 1 } moe_act_t;
 /* moe_expert_ffn that also keeps what the backward pass reads:
  *   x_perm [R, D], expert_off [E+1] (R = T*k)
  *   -> gu [R, 2, F] in dtype: row r holds g (biases added, before the clips),
- *      then u; a bf16 value is rounded to nearest but never across a clip bound,
+ *      then u; a bf16 value is rounded to nearest but never across a clip bound
+ *      (a negative g that would round to -0 stays the smallest negative value),
  *      so that the backward pass sees on which side of the clip it was,
- *      h [R, F] in dtype, y_perm [R, D] in dtype.
+ *      h [R, F] in dtype (rounded so before the down product reads it), y_perm
+ *      [R, D] in dtype.
  * Dense weights in dtype; each of the biases may be NULL (none).  h_split and
  * MXFP4 weights: MOE_ERR_UNSUPPORTED.  With E = k = 1 it is a dense block.  Rows
  * that belong to no expert (behind expert_off[E]) are left as they are.  A NaN
@@ -469,7 +471,10 @@ MOE_API moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, int32_t ac
 /* Backward pass of moe_combine: dy [T, D] in dtype (the gradient of y), the
  * forward's y_perm [T*k, D], row_of_slot [T, k] and topk_w [T, k]
  *   -> dy_perm [T*k, D] in dtype: dy_perm[row_of_slot[t,j]] = topk_w[t,j] dy[t],
- *      dtopk_w [T, k] fp32:       dtopk_w[t,j] = dy[t] . y_perm[row_of_slot[t,j]]. */
+ *      dtopk_w [T, k] fp32:       dtopk_w[t,j] = dy[t] . y_perm[row_of_slot[t,j]].
+ * dy is in dtype where y_f32 asked moe_combine for an fp32 y, too.  row_of_slot names
+ * every row once, as moe_permute leaves it: a row named twice gets pieces of
+ * either product, not their sum, and a row not named is left as it is. */
 MOE_API moe_status_t moe_combine_backward(const moe_config_t* cfg, int64_t T, const void* dy, const void* y_perm,
                                           const int32_t* row_of_slot, const float* topk_w, void* dy_perm,
                                           float* dtopk_w, void* stream);

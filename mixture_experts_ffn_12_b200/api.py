@@ -584,7 +584,7 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] 
                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[r] = q(x)[r] W_g^T + bias_g for the rows r of group g (group_off as expert_off; all rows if None),
     x quantized to MXFP4 in the call: 4-bit x 4-bit products on the block-scaled tensor cores
-    (moe_mxfp4_linear)."""
+    (moe_mxfp4_linear).  Rows of no group are not written: those of a new y hold anything."""
     R = check_mxfp4_linear_args(x, w, bias, group_off, y, out_f32)
     G, N, K = _mxfp4_sizes(w.codes)
     L, dev = _lib.load(), x.device
@@ -598,7 +598,8 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Weights, bias: Optional[torch.Tensor] 
 
 def quantize_experts(cfg: MoeConfig, w: ExpertWeights, wfmt: str = "mxfp4") -> Tuple[MoeConfig, ExpertWeights]:
     """Dense bf16 expert weights -> (config, weights) of the same layer with MXFP4 weights (wfmt "mxfp4"
-    or "mxfp4_a8"); biases stay as they are."""
+    or "mxfp4_a8"); biases stay as they are.  h_split does not carry over: layers with MXFP4 weights keep
+    h in bf16 ("mxfp4") or MXFP8 ("mxfp4_a8")."""
     if cfg.wfmt != _lib.MOE_W_DENSE or cfg.dtype != _lib.MOE_BF16:
         raise ValueError("quantize_experts takes dense bf16 expert weights")
     if wfmt not in ("mxfp4", "mxfp4_a8"):
@@ -652,7 +653,9 @@ def check_ffn_train_args(cfg: MoeConfig, x_perm, expert_off, w: ExpertWeights, g
 def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Tensor, weights: ExpertWeights,
                      act: str = "swiglu") -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """expert_ffn that also keeps the pre-activations: (gu [R, 2, F], h [R, F], y_perm [R, D]).
-    act: "swiglu" (the layer's clipped SwiGLU) or "silu"; biases may be None."""
+    act: "swiglu" (the layer's clipped SwiGLU) or "silu"; biases may be None.  Rows of no expert are not
+    written and hold anything.  A call of its own, which autograd does not see: expert_ffn_backward is its
+    backward pass."""
     code = _act_code(act)
     T = check_ffn_train_args(cfg, x_perm, expert_off, weights)
     R, dev, dt = x_perm.shape[0], x_perm.device, x_perm.dtype
@@ -687,7 +690,8 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
                         ws: Optional[torch.Tensor] = None) -> Tuple[Optional[torch.Tensor], ExpertGrads]:
     """Backward pass of expert_ffn_train: (dx_perm [R, D] or None, ExpertGrads).  Bias gradients come for
     the biases that `weights` has.  grad_f32: the parameters' gradients in fp32.  `grads` are buffers to
-    overwrite (same layouts, one dtype), else new ones."""
+    overwrite (same layouts, one dtype), else new ones.  dx_perm's rows of no expert are not written and hold
+    anything."""
     code = _act_code(act)
     if dy_perm is None:
         raise ValueError("dy_perm is required")
@@ -718,7 +722,8 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
 
 def combine_backward(cfg: MoeConfig, dy: torch.Tensor, y_perm: torch.Tensor, row_of_slot: torch.Tensor,
                      topk_w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Backward pass of combine: dy [T, D] (layer dtype) -> (dy_perm [T*k, D], dtopk_w [T, k] fp32)."""
+    """Backward pass of combine: dy [T, D] (layer dtype, with y_f32 too) -> (dy_perm [T*k, D], dtopk_w [T, k]
+    fp32).  row_of_slot names every row once, as permute leaves it."""
     T = check_combine_args(cfg, y_perm, row_of_slot, topk_w)
     dev = y_perm.device
     _want("dy", dy, (T, cfg.hidden_size), torch_dtype(cfg), dev)
