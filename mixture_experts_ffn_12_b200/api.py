@@ -670,10 +670,10 @@ def expert_ffn_train(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.Ten
 
 @dataclasses.dataclass
 class ExpertGrads:
-    """Gradients of the expert parameters, laid out as the parameters (moe_expert_grads_t)."""
-    w_gate: torch.Tensor
-    w_up: torch.Tensor
-    w_down: torch.Tensor
+    """Gradients of the expert parameters, laid out as the parameters (moe_expert_grads_t); None: not wanted."""
+    w_gate: Optional[torch.Tensor]
+    w_up: Optional[torch.Tensor]
+    w_down: Optional[torch.Tensor]
     b_gate: Optional[torch.Tensor] = None
     b_up: Optional[torch.Tensor] = None
     b_down: Optional[torch.Tensor] = None
@@ -690,7 +690,8 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
                         ws: Optional[torch.Tensor] = None) -> Tuple[Optional[torch.Tensor], ExpertGrads]:
     """Backward pass of expert_ffn_train: (dx_perm [R, D] or None, ExpertGrads).  Bias gradients come for
     the biases that `weights` has.  grad_f32: the parameters' gradients in fp32.  `grads` are buffers to
-    overwrite (same layouts, one dtype), else new ones.  dx_perm's rows of no expert are not written and hold
+    overwrite (same layouts, one dtype; a weight's or bias's may be None: not computed, as for frozen experts; a
+    bias's comes with its weight's), else new ones.  dx_perm's rows of no expert are not written and hold
     anything."""
     code = _act_code(act)
     if dy_perm is None:
@@ -704,13 +705,15 @@ def expert_ffn_backward(cfg: MoeConfig, x_perm: torch.Tensor, expert_off: torch.
         grads = ExpertGrads(*(None if p is None else like(p) for p in (
             weights.w_gate, weights.w_up, weights.w_down, weights.b_gate, weights.b_up, weights.b_down)))
     else:
-        for name, t, shape in (("grads.w_gate", grads.w_gate, (E, F, D)), ("grads.w_up", grads.w_up, (E, F, D)),
-                               ("grads.w_down", grads.w_down, (E, D, F))):
-            _want(name, t, shape, gdt, dev)
-        for name, t, n in (("grads.b_gate", grads.b_gate, F), ("grads.b_up", grads.b_up, F),
-                           ("grads.b_down", grads.b_down, D)):
+        for name, t, bias, shape in (("gate", grads.w_gate, grads.b_gate, (E, F, D)),
+                                     ("up", grads.w_up, grads.b_up, (E, F, D)),
+                                     ("down", grads.w_down, grads.b_down, (E, D, F))):
             if t is not None:
-                _want(name, t, (E, n), gdt, dev)
+                _want("grads.w_" + name, t, shape, gdt, dev)
+            if bias is not None:
+                if t is None:
+                    raise ValueError(f"grads.b_{name} is given without grads.w_{name}")
+                _want("grads.b_" + name, bias, shape[:2], gdt, dev)
     dx = torch.empty_like(x_perm) if need_dx else None
     ws = _workspace(ws, _size(L.moe_expert_ffn_backward_workspace_size(ctypes.byref(cfg), T),
                               "moe_expert_ffn_backward_workspace_size"), dev)

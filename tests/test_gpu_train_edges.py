@@ -220,3 +220,28 @@ def test_combine_backward_16_bytes_off(api, dtype):
     torch.cuda.synchronize()
     assert api.last_device_error() == 0
     assert all(torch.equal(a, c) for a, c in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("wanted", [(), ("w_down",), ("w_gate", "b_gate"), ("w_up", "w_down", "b_down")], ids=str)
+def test_some_gradients_only(api, wanted, dtype):
+    """The gradients that `grads` has buffers for, and dx or not: the bits of the whole pass, and no launch for what is
+    not wanted (dH, dX and the weights' gradients are one each)."""
+    from mixture_experts_ffn_12_b200 import _lib
+    from train_util import Block
+    b = Block([37, 0, 190], 96, 112, dtype, True, seed=13)
+    cfg, w = b.config(api), b.weights(api)
+    gu, h, _ = api.expert_ffn_train(cfg, b.x, b.off_gpu, w)
+    dx, full = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy)
+    names = ("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down")
+    for need_dx in (True, False):
+        some = api.ExpertGrads(*(torch.full_like(getattr(full, n), 7.0) if n in wanted else None for n in names))
+        before = _lib.load().moe_launch_count()
+        dx2, got = api.expert_ffn_backward(cfg, b.x, b.off_gpu, w, gu, h, b.dy, need_dx=need_dx, grads=some)
+        dh = need_dx or "w_gate" in wanted or "w_up" in wanted
+        assert _lib.load().moe_launch_count() - before == dh + need_dx + bool(wanted)
+        torch.cuda.synchronize()
+        assert api.last_device_error() == 0
+        assert torch.equal(dx, dx2) if need_dx else dx2 is None
+        for n in names:
+            assert torch.equal(getattr(got, n), getattr(full, n)) if n in wanted else getattr(got, n) is None
