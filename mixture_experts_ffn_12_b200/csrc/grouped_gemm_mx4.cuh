@@ -26,7 +26,8 @@
 // the time, 237 MB from and to HBM), 128 rows 24 us (5.9 TB/s of weights: HBM).  At 16384 rows one
 // launch alone, at 1.6 to 1.9 GHz, is not bound by power: at the tensor pipe's nominal rate a
 // stage's 31 KB a CTA in 384 cycles would ask some 21 TB/s of the L2, more than it was seen to give
-// (15.5), and a wider tile has no room in TMEM beside two scale sets.  Single CTAs with the rows in M took 125 and 41 us.
+// (15.5), and a wider tile has no room in TMEM beside two scale sets.  Single CTAs with the rows
+// in M took 125 and 41 us.
 #pragma once
 
 #include "mxfp4_quant.cuh"
